@@ -25,7 +25,12 @@
  *     (dllm_prepare_rows, dllm_masked_logits_prepared);
  *   - a vocabulary-parallel LM head over several GPUs: per-shard softmax partials and their
  *     merge (dllm_masked_partials, dllm_lse_merge);
- *   - compaction without a workspace (dllm_mask_compact_noalloc).
+ *   - compaction without a workspace (dllm_mask_compact_noalloc);
+ *   - rules on the logits - penalties for repeated tokens, biases, grammar bitmaps - applied in
+ *     the LM head's epilogue (dllm_masked_logits_rules) and the token counts that the
+ *     penalties read (dllm_token_counts);
+ *   - the LM head with W and the masked rows in microscaled 4-bit floating point
+ *     (dllm_mx4_quantize, dllm_mx4_dequantize, dllm_masked_logits_mx4).
  *
  * Conventions for every call:
  *   - Pointers marked "device" must point to memory of the current CUDA device; the caller
@@ -453,6 +458,142 @@ dllm_status dllm_decode_block_step(const uint16_t* H, const uint8_t* M, const ui
                                    int32_t* row_idx, int32_t* seq_off, int32_t* count,
                                    int32_t* idx, int32_t* n_sel, int32_t* tok_sel,
                                    float* conf_sel, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * dllm_logit_rules - rules on the logits of the masked rows, for dllm_masked_logits_rules and
+ * dllm_masked_logits_mx4.  For the masked position (b, l) and token v with raw logit z0:
+ *     c  = counts[b, v]
+ *     z1 = c > 0 ? (z0 > 0 ? z0 / repetition[b] : z0 * repetition[b])
+ *                  - presence[b] - frequency[b] * c                  : z0
+ *     z2 = z1 + bias[b, v]
+ *     z  = allowed ? z2 : -infinity
+ * and tok, lse, conf and the scores are those of z (fp32, one rounding per step).  Every
+ * pointer may be NULL: without counts no penalty applies, a NULL penalty is neutral
+ * (repetition 1, presence 0, frequency 0).  The struct is read during the call; what its
+ * pointers name is read by the kernels.
+ *
+ *   bias        device float32; sequence b's row starts at bias + b * bias_stride (0: one row
+ *               for every sequence; else a multiple of 4, >= V).  -infinity bans a token; the
+ *               lowest finite value is a number like any other.  NaN and +infinity are not
+ *               allowed, except where the bitmap bans the token anyway.
+ *   counts      device int32 [B] rows of V, counts_stride apart (>= V): how often each token
+ *               stands in each sequence (dllm_token_counts).
+ *   seen        device bitmap of counts > 0: bit v % 32 of word v / 32, rows seen_stride words
+ *               apart (>= ceil(V / 32)).  Required with counts; counts are read only where its
+ *               bit is set.
+ *   repetition, presence, frequency   device float32 [B]; repetition > 0.  They require counts.
+ *   allow       device bitmaps of allowed tokens: allow_rows rows of ceil(V / 32) words,
+ *               allow_stride words apart; bit set = allowed.
+ *   allow_id    device int32 [B * L]: the bitmap of each position, negative = unrestricted; a
+ *               number >= allow_rows is recorded as DLLM_ERR_BOUNDS and the row is left
+ *               unrestricted.  NULL: bitmap 0 for all if allow_rows == 1, else bitmap b
+ *               (allow_rows == B).
+ *
+ * A row with no token left (every z = -infinity): tok = -1, conf = 0, lse = -infinity,
+ * entropy = +infinity, margin = 0.  A selection takes such a row after all others.
+ */
+typedef struct dllm_logit_rules {
+  const float* bias;
+  int64_t bias_stride;
+  const int32_t* counts;
+  int64_t counts_stride;
+  const uint32_t* seen;
+  int64_t seen_stride;
+  const float* repetition;
+  const float* presence;
+  const float* frequency;
+  const uint32_t* allow;
+  int64_t allow_stride;
+  const int32_t* allow_id;
+  int32_t allow_rows;
+} dllm_logit_rules;
+
+/*
+ * dllm_masked_logits_rules - dllm_masked_logits_window (or, with both windows NULL,
+ * dllm_masked_logits_ex) with rules on the logits.  The rules are applied to the accumulators
+ * in the GEMM epilogue; no logit is stored.  rules is a host pointer, required.  Other
+ * arguments, outputs and errors as in dllm_masked_logits_window; further errors:
+ * DLLM_ERR_NULL (counts without seen or seen without counts, a penalty without counts,
+ * allow_id without allow), DLLM_ERR_ALIGN (a pointer that is not 16-byte aligned),
+ * DLLM_ERR_SHAPE (a stride too small, bias_stride not a multiple of 4, allow_rows < 1 or, without allow_id,
+ * neither 1 nor B).
+ */
+dllm_status dllm_masked_logits_rules(const uint16_t* H, const uint8_t* M, const uint16_t* W,
+                                     int32_t B, int32_t L, int32_t d, int32_t V,
+                                     const int32_t* win_lo, const int32_t* win_hi,
+                                     const dllm_logit_rules* rules, uint32_t stats, int32_t* tok,
+                                     float* conf, float* lse, float* entropy, float* margin,
+                                     int32_t* row_idx, int32_t* seq_off, int32_t* count, void* ws,
+                                     size_t ws_bytes, void* stream);
+
+/*
+ * dllm_token_counts - how often each token stands in each sequence (dllm_logit_rules).
+ *
+ *   tokens   device int32 [B, n] row-major; ids outside [0, V) are skipped.
+ *   M        device uint8 [B, n] or NULL: positions with a nonzero byte (still masked) are
+ *            skipped.
+ *   n_valid  device int32 [B] or NULL: only the first n_valid[b] tokens of sequence b count.
+ *   accumulate  0: counts and seen are written for all V tokens.  1: the tokens are added to
+ *            counts and seen that an earlier call wrote; with tokens = tok_sel [B, k] and
+ *            n_valid = n_sel of a selection, those a step has just unmasked.
+ *   counts   device int32 [B, V].      seen  device uint32 [B, ceil(V / 32)].
+ * tokens may be NULL if n == 0.  Errors: DLLM_ERR_NULL, DLLM_ERR_ALIGN, DLLM_ERR_SHAPE (B < 1,
+ * B > 65535, n < 0, V < 1, accumulate not 0/1), DLLM_ERR_CUDA, DLLM_ERR_DEVICE.
+ */
+dllm_status dllm_token_counts(const int32_t* tokens, const uint8_t* M, const int32_t* n_valid,
+                              int32_t B, int32_t n, int32_t V, int32_t accumulate,
+                              int32_t* counts, uint32_t* seen, void* stream);
+
+/*
+ * dllm_mx4_quantize / dllm_mx4_dequantize - microscaled 4-bit floating point (MXFP4 of the OCP
+ * Microscaling Formats specification v1.0): blocks of 32 consecutive elements of a row share
+ * a scale 2^e (E8M0), each element is an E2M1 code.
+ *     e    = max(floor(log2 max|x|) - 2, -127)
+ *     code = the E2M1 value nearest to x / 2^e, ties to the even code, at most 6 in size
+ * A block holding a NaN or an infinity gets the NaN scale.
+ *
+ *   X        device [rows, cols], row stride ld >= cols elements; dtype DLLM_BF16, DLLM_F16 or
+ *            DLLM_F32 (dequantize: DLLM_BF16 or DLLM_F32, both exact).  Rows must start on 16
+ *            bytes (ld a multiple of 8, or of 4 for DLLM_F32).
+ *   q        device uint8 [rows, cols / 2], element 2i in the low nibble of byte i.
+ *   s        device uint8, dllm_mx4_scale_bytes(rows, cols) bytes: scale bytes (2^(s - 127),
+ *            0xFF = NaN) in tiles of 128 rows by 4 blocks; the byte of row r, block j = k / 32
+ *            is at ((r / 128) * ceil(cols / 128) + j / 4) * 512 + (r % 32) * 16
+ *            + ((r / 32) % 4) * 4 + j % 4; the rest of the tiles holds 0.
+ * Constraints: rows >= 1, cols a positive multiple of 32.  Errors: DLLM_ERR_NULL,
+ * DLLM_ERR_ALIGN, DLLM_ERR_SHAPE, DLLM_ERR_CUDA, DLLM_ERR_DEVICE.
+ */
+#define DLLM_BF16 0
+#define DLLM_F16  1
+#define DLLM_F32  2
+size_t dllm_mx4_scale_bytes(int64_t rows, int32_t cols);      /* 0 for invalid shapes */
+dllm_status dllm_mx4_quantize(const void* X, int32_t dtype, int64_t rows, int32_t cols, int64_t ld,
+                              uint8_t* q, uint8_t* s, void* stream);
+dllm_status dllm_mx4_dequantize(const uint8_t* q, const uint8_t* s, int64_t rows, int32_t cols,
+                                int32_t dtype, void* X, int64_t ld, void* stream);
+
+/*
+ * dllm_masked_logits_mx4 - the mask-only LM head in MXFP4: W is an MXFP4 matrix [V, d]
+ * (dllm_mx4_quantize, once per model), the masked rows of H are quantised to MXFP4 as they
+ * are gathered, and the products run on the 4-bit block-scaled tensor cores with fp32
+ * accumulation.  Against dllm_masked_logits this reads 0.53 instead of 2 bytes per element of
+ * W.  The rules (nullable) and statistics are those of dllm_masked_logits_rules.
+ *
+ *   Wq, Ws   device: codes and scales of W.
+ *   ws       device workspace of dllm_workspace_bytes_mx4(B, L, d, V, max_rows) bytes; as with
+ *            the bf16 calls a smaller one than for max_rows = B*L holds the masked rows that
+ *            fit (dllm_workspace_rows_mx4) and more of them record DLLM_ERR_CAPACITY.
+ * Other arguments, constraints and errors as in dllm_masked_logits_rules.
+ */
+size_t dllm_workspace_bytes_mx4(int32_t B, int32_t L, int32_t d, int32_t V, int64_t max_rows);
+int64_t dllm_workspace_rows_mx4(int32_t B, int32_t L, int32_t d, int32_t V, size_t ws_bytes);
+dllm_status dllm_masked_logits_mx4(const uint16_t* H, const uint8_t* M, const uint8_t* Wq,
+                                   const uint8_t* Ws, int32_t B, int32_t L, int32_t d, int32_t V,
+                                   const int32_t* win_lo, const int32_t* win_hi,
+                                   const dllm_logit_rules* rules, uint32_t stats, int32_t* tok,
+                                   float* conf, float* lse, float* entropy, float* margin,
+                                   int32_t* row_idx, int32_t* seq_off, int32_t* count, void* ws,
+                                   size_t ws_bytes, void* stream);
 
 /*
  * dllm_get_status - synchronise `stream`, then return (and clear) the device-side status

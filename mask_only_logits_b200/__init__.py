@@ -8,7 +8,10 @@ fallback: if ``libdllm.so`` is missing, loading fails loudly.
 Low-level calls (same names and arguments as the C ABI, tensors instead of pointers):
 ``workspace_bytes``, ``mask_compact``, ``masked_logits``, ``select_unmask``,
 ``decode_step``, ``get_status``, and for a vocabulary-parallel LM head ``masked_partials``
-and ``lse_merge``.  ``DecodeStep`` owns the buffers of one shape and runs a whole step on
+and ``lse_merge``.  Rules on the logits (``LogitRules``: penalties for repeated tokens, biases,
+grammar bitmaps) go into ``masked_logits_rules``, with ``token_counts`` for the penalties; a
+projection in microscaled 4-bit floating point (``Mx4Matrix``) into ``masked_logits_mx4``.
+``DecodeStep`` takes both (``run(..., rules=...)``, ``weights="mx4"``); it owns the buffers of one shape and runs a whole step on
 device tensors (``run``) or on host tensors with the copies included (``run_host``,
 ``run_host_pipeline``); ``sharded.VocabShardedStep`` runs it with W split over ranks.
 """
@@ -28,6 +31,9 @@ __all__ = [
     "select_unmask", "decode_step", "get_status", "debug_lmhead_logits", "debug_lse_merge",
     "debug_set_gemm_variant",
     "prof_begin", "prof_end", "DecodeStep", "MAX_K",
+    "LogitRules", "masked_logits_rules", "token_counts",
+    "Mx4Matrix", "mx4_scale_bytes", "mx4_quantize", "mx4_dequantize", "mx4_tile_scales",
+    "mx4_row_scales", "masked_logits_mx4", "workspace_bytes_mx4", "workspace_rows_mx4",
 ]
 
 MAX_K = 1024
@@ -406,6 +412,267 @@ def decode_step(H, M, W, k, tok, conf, lse, row_idx, seq_off, count, idx, n_sel,
         _ptr(ws, None, "ws"), ws.numel() * ws.element_size(), _stream(stream)), name)
 
 
+# -- rules on the logits, MXFP4 operands ---------------------------------------------------
+def _bitmap_words(V: int) -> int:
+    return (V + 31) // 32
+
+
+def _same_device(**tensors) -> None:
+    """The library launches on the current device: every CUDA tensor must live there."""
+    cur = None
+    for name, t in tensors.items():
+        if t is not None and t.is_cuda:
+            if cur is None:
+                cur = torch.cuda.current_device()
+            if t.device.index != cur:
+                raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{cur}")
+
+
+def _rows_ptr(t, dtypes, name: str, rows: int, cols: int) -> tuple:
+    """(pointer, row stride) of a 2-D device tensor of at least `rows` x `cols` whose rows are
+    contiguous (views of wider buffers pass as they are)."""
+    if t.dim() != 2 or t.shape[0] < rows or t.shape[1] < cols:
+        raise ValueError(f"{name}: expected at least [{rows}, {cols}], got {list(t.shape)}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name}: expected {dtypes[0]}, got {t.dtype}")
+    if not _on_device(t, False):
+        raise ValueError(f"{name}: expected a CUDA tensor")
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: expected contiguous rows")
+    ld = t.stride(0) if t.shape[0] > 1 else max(cols, t.shape[1])
+    if ld < cols:
+        raise ValueError(f"{name}: rows overlap (stride {ld}, {cols} columns)")
+    return t.data_ptr(), ld
+
+
+class LogitRules:
+    """Rules on the logits of a step of shape (B, L, V): the tensors and their checked
+    description (``dllm_logit_rules``).  For token v at masked position (b, l) with raw logit
+    z and c = counts[b, v]:
+
+        where c > 0:   z / repetition[b] if z > 0 else z * repetition[b],
+                       then minus presence[b] + frequency[b] * c
+        plus bias[b, v]; -inf where the position's bitmap does not allow v.
+
+    bias        float32 [V], or [B, V] with a row stride that is a multiple of 4
+    counts      int32 [B, V], seen int32 [B, ceil(V / 32)]: see ``token_counts``
+    repetition, presence, frequency   float32 [B]; they need counts
+    allow       int32 [S, ceil(V / 32)]: S bitmaps, bit v % 32 of word v // 32 set = allowed
+    allow_id    int32 [B, L]: the bitmap of each position, negative = unrestricted; without
+                it bitmap b is sequence b's (S == B) or bitmap 0 everyone's (S == 1)
+
+    The tensors are read by the kernels of each step they are passed to: their contents may
+    change between steps (in stream order), their storage may not."""
+
+    def __init__(self, B: int, L: int, V: int, bias=None, counts=None, seen=None, repetition=None,
+                 presence=None, frequency=None, allow=None, allow_id=None):
+        self.B, self.L, self.V = int(B), int(L), int(V)
+        self.tensors = dict(bias=bias, counts=counts, seen=seen, repetition=repetition,
+                            presence=presence, frequency=frequency, allow=allow, allow_id=allow_id)
+        words, i32 = _bitmap_words(V), (torch.int32, torch.uint32)
+        if (counts is None) != (seen is None):
+            raise ValueError("counts and seen go together (token_counts writes both)")
+        if counts is None and any(t is not None for t in (repetition, presence, frequency)):
+            raise ValueError("penalties need counts and seen")
+        if allow_id is not None and allow is None:
+            raise ValueError("allow_id needs allow")
+        r = _abi.LogitRulesStruct()
+        if bias is not None:
+            if bias.dim() == 1:
+                r.bias, _ = _rows_ptr(bias[None], (torch.float32,), "bias", 1, V)
+            else:
+                r.bias, r.bias_stride = _rows_ptr(bias, (torch.float32,), "bias", B, V)
+                if B == 1:
+                    r.bias_stride = 0
+                elif r.bias_stride % 4 != 0:
+                    raise ValueError(f"bias: row stride {r.bias_stride} is not a multiple of 4")
+        if counts is not None:
+            r.counts, r.counts_stride = _rows_ptr(counts, i32[:1], "counts", B, V)
+            r.seen, r.seen_stride = _rows_ptr(seen, i32, "seen", B, words)
+        for name in ("repetition", "presence", "frequency"):
+            t = self.tensors[name]
+            if t is not None:
+                setattr(r, name, _ptr(t, torch.float32, name, n=B).value)
+        if allow is not None:
+            r.allow, r.allow_stride = _rows_ptr(allow, i32, "allow", 1, words)
+            r.allow_rows = allow.shape[0]
+            if allow_id is not None:
+                r.allow_id = _ptr(allow_id, torch.int32, "allow_id", n=B * L).value
+            elif allow.shape[0] not in (1, B):
+                raise ValueError(f"allow: {allow.shape[0]} bitmaps for {B} sequences need allow_id")
+        self._struct = r
+
+    def _ref(self, B: int, L: int, V: int):
+        if (B, L, V) != (self.B, self.L, self.V):
+            raise ValueError(f"rules: made for (B, L, V) = {(self.B, self.L, self.V)}, "
+                             f"used with {(B, L, V)}")
+        _same_device(**self.tensors)
+        return ctypes.byref(self._struct)
+
+
+def token_counts(tokens, counts, seen, M=None, n_valid=None, accumulate=False, stream=None) -> None:
+    """counts[b, v] = how often token v stands in tokens[b] (int32 [B, n]), at positions whose
+    mask byte M[b, j] is zero (M given) and among the first n_valid[b] (n_valid given); seen =
+    the bitmap of counts > 0.  With accumulate=True the tokens are added to both: after a
+    step, ``token_counts(tok_sel, counts, seen, n_valid=n_sel, accumulate=True)`` adds what it
+    unmasked.  Ids outside [0, V) are skipped."""
+    B, n = tokens.shape
+    V = counts.shape[-1]
+    if tuple(counts.shape) != (B, V) or tuple(seen.shape) != (B, _bitmap_words(V)):
+        raise ValueError(f"counts, seen: expected [{B}, V] and [{B}, ceil(V / 32)], got "
+                         f"{list(counts.shape)} and {list(seen.shape)}")
+    if seen.dtype not in (torch.int32, torch.uint32):
+        raise ValueError(f"seen: expected torch.int32, got {seen.dtype}")
+    _same_device(tokens=tokens, counts=counts, seen=seen, M=M, n_valid=n_valid)
+    _check(lib().dllm_token_counts(
+        _ptr(tokens, torch.int32, "tokens"), _ptr(M, torch.uint8, "M", n=B * n),
+        _ptr(n_valid, torch.int32, "n_valid", n=B), B, n, V, 1 if accumulate else 0,
+        _ptr(counts, torch.int32, "counts"), _ptr(seen, None, "seen"), _stream(stream)),
+        "dllm_token_counts")
+
+
+def _shaped_args(H, M, stats, tok, conf, lse, entropy, margin, row_idx, seq_off, count, ws,
+                 win_lo, win_hi, d: int) -> tuple:
+    """(pointers of H and M; of the windows; of the outputs, workspace and its size)."""
+    B, L = M.shape
+    n = B * L
+    _same_device(H=H, M=M, tok=tok, conf=conf, lse=lse, entropy=entropy, margin=margin,
+                 row_idx=row_idx, seq_off=seq_off, count=count, ws=ws, win_lo=win_lo, win_hi=win_hi)
+    return ((_ptr(H, torch.bfloat16, "H", True, n * d), _ptr(M, torch.uint8, "M", True)),
+            (_ptr(win_lo, torch.int32, "win_lo", n=B), _ptr(win_hi, torch.int32, "win_hi", n=B)),
+            (_ptr(tok, torch.int32, "tok", n=n), _ptr(conf, torch.float32, "conf", n=n),
+             _ptr(lse, torch.float32, "lse", n=n), _ptr(entropy, torch.float32, "entropy", n=n),
+             _ptr(margin, torch.float32, "margin", n=n), _ptr(row_idx, torch.int32, "row_idx", n=n),
+             _ptr(seq_off, torch.int32, "seq_off", n=B + 1), _ptr(count, torch.int32, "count", n=1),
+             _ptr(ws, None, "ws"), ws.numel() * ws.element_size()))
+
+
+def masked_logits_rules(H, M, W, rules: LogitRules, stats, tok, conf, lse, entropy, margin, row_idx,
+                        seq_off, count, ws, stream=None, win_lo=None, win_hi=None) -> None:
+    """masked_logits_ex with rules on the logits (applied in the GEMM epilogue).  A row with no
+    token left gets tok -1, conf 0, lse -inf, entropy +inf, margin 0."""
+    B, L = M.shape
+    V, d = W.shape
+    _same_device(W=W)
+    ins, win, outs = _shaped_args(H, M, stats, tok, conf, lse, entropy, margin, row_idx, seq_off,
+                                  count, ws, win_lo, win_hi, d)
+    _check(lib().dllm_masked_logits_rules(*ins, _ptr(W, torch.bfloat16, "W"), B, L, d, V, *win,
+                                          rules._ref(B, L, V), stats, *outs, _stream(stream)),
+           "dllm_masked_logits_rules")
+
+
+_MX4_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def mx4_scale_bytes(rows: int, cols: int) -> int:
+    """Bytes of the scales of an MXFP4 matrix (0 for invalid shapes)."""
+    return int(lib().dllm_mx4_scale_bytes(rows, cols))
+
+
+def _mx4_args(X, q, s, dtypes) -> tuple:
+    rows, cols = X.shape
+    if cols % 32 != 0 or cols == 0:
+        raise ValueError(f"X: {cols} columns are not a positive multiple of 32")
+    ptr, ld = _rows_ptr(X, dtypes, "X", rows, cols)
+    _same_device(X=X, q=q, s=s)
+    return (ctypes.c_void_p(ptr), _MX4_DTYPES[X.dtype], rows, cols, ld,
+            _ptr(q, torch.uint8, "q", n=rows * (cols // 2)),
+            _ptr(s, torch.uint8, "s", n=-(-rows // 128) * -(-cols // 128) * 512))
+
+
+def mx4_quantize(X, q, s, stream=None) -> None:
+    """X [rows, cols] (bf16, fp16 or fp32; rows may be strided) to MXFP4: codes q uint8
+    [rows, cols / 2] and scales s uint8 [mx4_scale_bytes(rows, cols)]."""
+    ptr, dt, rows, cols, ld, qp, sp = _mx4_args(X, q, s, (torch.bfloat16, torch.float16, torch.float32))
+    _check(lib().dllm_mx4_quantize(ptr, dt, rows, cols, ld, qp, sp, _stream(stream)),
+           "dllm_mx4_quantize")
+
+
+def mx4_dequantize(q, s, X, stream=None) -> None:
+    """The values that codes q and scales s stand for, into X [rows, cols] (bf16 or fp32, both
+    exact)."""
+    ptr, dt, rows, cols, ld, qp, sp = _mx4_args(X, q, s, (torch.bfloat16, torch.float32))
+    _check(lib().dllm_mx4_dequantize(qp, sp, rows, cols, dt, ptr, ld, _stream(stream)),
+           "dllm_mx4_dequantize")
+
+
+def mx4_tile_scales(scales: torch.Tensor) -> torch.Tensor:
+    """Row-major E8M0 scales [rows, cols / 32] (as MXFP4 checkpoints store them) in the
+    library's tiles of 128 rows x 4 blocks."""
+    rows, blocks = scales.shape
+    R, G = -(-rows // 128), -(-blocks // 4)
+    full = torch.zeros(R * 128, G * 4, dtype=torch.uint8, device=scales.device)
+    full[:rows, :blocks] = scales
+    # [tile row, row / 32 % 4, row % 32, tile column, block % 4] -> the tile's byte order
+    return full.view(R, 4, 32, G, 4).permute(0, 3, 2, 1, 4).reshape(-1).contiguous()
+
+
+def mx4_row_scales(s: torch.Tensor, rows: int, cols: int) -> torch.Tensor:
+    """The inverse of mx4_tile_scales: row-major E8M0 scales [rows, cols / 32]."""
+    R, G = -(-rows // 128), -(-cols // 128)
+    full = s[:R * G * 512].view(R, G, 32, 4, 4).permute(0, 3, 2, 1, 4).reshape(R * 128, G * 4)
+    return full[:rows, :cols // 32].contiguous()
+
+
+class Mx4Matrix:
+    """An MXFP4 matrix [rows, cols] on the GPU: codes ``q`` uint8 [rows, cols / 2] and scales
+    ``s`` uint8 (the library's tiles).  ``quantize`` makes one from a dense matrix."""
+
+    def __init__(self, q: torch.Tensor, s: torch.Tensor):
+        if q.dim() != 2 or q.dtype != torch.uint8 or q.shape[0] < 1 or q.shape[1] % 16 or q.shape[1] == 0:
+            raise ValueError("q: expected uint8 [rows, cols / 2] with cols a multiple of 32")
+        self.rows, self.cols = q.shape[0], q.shape[1] * 2
+        n = -(-self.rows // 128) * -(-self.cols // 128) * 512
+        if s.dtype != torch.uint8 or s.numel() < n:
+            raise ValueError(f"s: expected uint8 of at least {n} bytes")
+        self.q, self.s = q, s
+
+    @property
+    def shape(self) -> tuple:
+        return (self.rows, self.cols)
+
+    @classmethod
+    def quantize(cls, X: torch.Tensor, stream=None) -> "Mx4Matrix":
+        rows, cols = X.shape
+        q = torch.empty(rows, cols // 2, dtype=torch.uint8, device=X.device)
+        s = torch.empty(-(-rows // 128) * -(-cols // 128) * 512, dtype=torch.uint8, device=X.device)
+        mx4_quantize(X, q, s, stream)
+        return cls(q, s)
+
+    def dequantize(self, dtype=torch.bfloat16, stream=None) -> torch.Tensor:
+        X = torch.empty(self.rows, self.cols, dtype=dtype, device=self.q.device)
+        mx4_dequantize(self.q, self.s, X, stream)
+        return X
+
+
+def workspace_bytes_mx4(B: int, L: int, d: int, V: int, max_rows: int | None = None) -> int:
+    """Workspace bytes of masked_logits_mx4 for at most max_rows masked rows (default B * L;
+    0 if invalid)."""
+    return int(lib().dllm_workspace_bytes_mx4(B, L, d, V, B * L if max_rows is None else max_rows))
+
+
+def workspace_rows_mx4(B: int, L: int, d: int, V: int, ws_bytes: int) -> int:
+    """Masked-row capacity of a masked_logits_mx4 workspace of ws_bytes."""
+    return int(lib().dllm_workspace_rows_mx4(B, L, d, V, ws_bytes))
+
+
+def masked_logits_mx4(H, M, W: Mx4Matrix, rules: LogitRules | None, stats, tok, conf, lse, entropy,
+                      margin, row_idx, seq_off, count, ws, stream=None, win_lo=None,
+                      win_hi=None) -> None:
+    """masked_logits_ex with W in MXFP4 and the masked rows of H quantised to it as they are
+    gathered (block-scaled 4-bit tensor-core products, fp32 accumulation), with rules on the
+    logits if given.  ws: workspace_bytes_mx4 bytes."""
+    B, L = M.shape
+    V, d = W.shape
+    _same_device(Wq=W.q, Ws=W.s)
+    ins, win, outs = _shaped_args(H, M, stats, tok, conf, lse, entropy, margin, row_idx, seq_off,
+                                  count, ws, win_lo, win_hi, d)
+    _check(lib().dllm_masked_logits_mx4(
+        *ins, _ptr(W.q, torch.uint8, "Wq"), _ptr(W.s, torch.uint8, "Ws"), B, L, d, V, *win,
+        None if rules is None else rules._ref(B, L, V), stats, *outs, _stream(stream)),
+        "dllm_masked_logits_mx4")
+
+
 def get_status(stream=None) -> int:
     return int(lib().dllm_get_status(_stream(stream)))
 
@@ -467,13 +734,20 @@ class DecodeStep:
     unmasked, at most k and at least min(min_sel, candidates) per sequence; without it, the k
     best.  ``conf_sel`` then holds the policy's score of each selected position.
 
+    ``weights="mx4"``: W is an ``Mx4Matrix`` and the LM head runs in MXFP4.  ``run``,
+    ``run_host`` and ``capture`` take ``rules`` (``LogitRules``) with either kind of weights; a
+    selected position whose rules leave no token has tok_sel -1.
+
     Outputs are views into buffers owned by this object; their first ``count`` entries are
     valid (``count`` stays on the device unless read).
     """
 
     def __init__(self, B: int, L: int, d: int, V: int, k: int, device="cuda",
                  policy: str = "confidence", threshold: float | None = None, min_sel: int = 1,
-                 arena: bool = False, arena_chunk: int = 0):
+                 arena: bool = False, arena_chunk: int = 0, weights: str = "bf16"):
+        if weights not in ("bf16", "mx4"):
+            raise ValueError("weights must be 'bf16' or 'mx4'")
+        self.weights = weights
         if k < 1 or k > MAX_K:
             raise ValueError(f"k must be in [1, {MAX_K}]")
         if policy not in POLICIES:
@@ -502,7 +776,7 @@ class DecodeStep:
             self._sel_off.append(self._sel_off[-1] + (n_part + 3) // 4 * 4)
         self.sel_buf = torch.empty(self._sel_off[-1], **i32)
         self.idx, self.n_sel, self.tok_sel, self.conf_sel = self._sel_views(self.sel_buf)
-        nbytes = workspace_bytes(B, L, d, V)
+        nbytes = workspace_bytes_mx4(B, L, d, V) if weights == "mx4" else workspace_bytes(B, L, d, V)
         if nbytes == 0:
             raise ValueError("invalid shapes (d must be a positive multiple of 64)")
         # arena=True: the workspace lives in an Arena whose mapping follows each step's
@@ -516,7 +790,8 @@ class DecodeStep:
         (growing or shrinking the arena's backing); returns the bytes that step needs."""
         if self.arena is None:
             raise RuntimeError("size_for_rows needs DecodeStep(..., arena=True)")
-        need = workspace_bytes_rows(self.B, self.L, self.d, self.V, max(1, int(max_rows)))
+        sizer = workspace_bytes_mx4 if self.weights == "mx4" else workspace_bytes_rows
+        need = sizer(self.B, self.L, self.d, self.V, max(1, int(max_rows)))
         if self.ws is None or self.arena.mapped != -(-need // self.arena.chunk) * self.arena.chunk:
             self.arena.map(need)
         self.ws = self.arena.tensor()
@@ -542,6 +817,8 @@ class DecodeStep:
     def _check_W(self, W) -> None:
         """W must be this step's [V, d] projection: the staging and the GEMM halves of a step
         take their shapes from this object and from W respectively."""
+        if isinstance(W, Mx4Matrix) != (self.weights == "mx4"):
+            raise ValueError("W: an Mx4Matrix needs DecodeStep(..., weights='mx4'), and the reverse")
         if tuple(W.shape) != (self.V, self.d):
             raise ValueError(f"W: expected shape ({self.V}, {self.d}), got {tuple(W.shape)}")
 
@@ -582,7 +859,7 @@ class DecodeStep:
         return out
 
     def run(self, H, M, W, win_lo=None, win_hi=None, stream=None, block_only=False,
-            max_rows: int | None = None) -> dict:
+            max_rows: int | None = None, rules: LogitRules | None = None) -> dict:
         """One step on device tensors.  block_only=True (windows required): logits for the
         masked rows inside the windows only; tok/conf/lse/row_idx then cover those rows.
         Arena mode: the workspace is mapped for max_rows masked rows first (a decoding loop
@@ -591,7 +868,15 @@ class DecodeStep:
         if self.arena is not None:
             self.size_for_rows(self._rows_of(M, win_lo, win_hi, block_only)
                                if max_rows is None else max_rows)
-        if self._plain():
+        if rules is not None or self.weights == "mx4":
+            if tuple(M.shape) != (self.B, self.L):
+                raise ValueError(f"M: expected shape ({self.B}, {self.L}), got {tuple(M.shape)}")
+            (masked_logits_mx4 if self.weights == "mx4" else masked_logits_rules)(
+                H, M, W, rules, self.stats, self.tok, self.conf, self.lse, self.entropy, self.margin,
+                self.row_idx, self.seq_off, self.count, self.ws, stream,
+                *((win_lo, win_hi) if block_only else (None, None)))
+            self._select(self.row_idx, self.seq_off, win_lo, win_hi, stream)
+        elif self._plain():
             decode_step(H, M, W, self.k, self.tok, self.conf, self.lse, self.row_idx,
                         self.seq_off, self.count, self.idx, self.n_sel, self.ws, win_lo, win_hi,
                         self.tok_sel, self.conf_sel, stream, block_only)
@@ -603,7 +888,7 @@ class DecodeStep:
         return self._outputs()
 
     # -- end-to-end from host memory ---------------------------------------------------------
-    def capture(self, H, M, W, win_lo=None, win_hi=None, block_only=False):
+    def capture(self, H, M, W, win_lo=None, win_hi=None, block_only=False, rules=None):
         """Capture one step on these device tensors into a CUDA graph.  ``replay()`` then
         reruns the whole step (every kernel, with the programmatic-launch edges between them)
         on whatever those tensors hold at replay time, for one launch of CPU work; the
@@ -617,11 +902,11 @@ class DecodeStep:
         side.wait_stream(torch.cuda.current_stream(self.device))
         with torch.cuda.stream(side):
             for _ in range(2):                   # one-time device set-up happens outside capture
-                self.run(H, M, W, win_lo, win_hi, side, block_only)
+                self.run(H, M, W, win_lo, win_hi, side, block_only, rules=rules)
         torch.cuda.current_stream(self.device).wait_stream(side)
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph, capture_error_mode="thread_local"):
-            self.run(H, M, W, win_lo, win_hi, None, block_only)
+            self.run(H, M, W, win_lo, win_hi, None, block_only, rules=rules)
         self._graph = graph
         return graph
 
@@ -646,7 +931,7 @@ class DecodeStep:
         return self._host
 
     def run_host(self, H_host, M_host, W, win_lo=None, win_hi=None, stream=None,
-                 block_only=False) -> dict:
+                 block_only=False, rules=None) -> dict:
         """One step from host H and M: copy them in, run, copy the selection back.
 
         W (the resident vocabulary projection) and the windows are device tensors.  Returns
@@ -659,7 +944,7 @@ class DecodeStep:
         with torch.cuda.stream(s):
             hb["H"].copy_(H_host, non_blocking=True)
             hb["M"].copy_(M_host, non_blocking=True)
-            self.run(hb["H"], hb["M"], W, win_lo, win_hi, s, block_only, max_rows=rows)
+            self.run(hb["H"], hb["M"], W, win_lo, win_hi, s, block_only, max_rows=rows, rules=rules)
             hb["sel"].copy_(self.sel_buf, non_blocking=True)
         s.synchronize()
         return dict(zip(("idx", "n_sel", "tok_sel", "conf_sel"), self._sel_views(hb["sel"])))
@@ -667,6 +952,9 @@ class DecodeStep:
     def _double(self) -> dict:
         """Two sets of (workspace, row_idx, seq_off, count): this object's own and a second
         one, so that staging of one step can run while the previous step computes."""
+        if self.weights == "mx4":
+            raise RuntimeError("the overlapped loops stage bf16 rows; with weights='mx4' run steps "
+                               "one at a time (run, run_host, capture)")
         if self.arena is not None:
             raise RuntimeError("the overlapped loops keep two fixed workspaces; with arena=True "
                                "run steps one at a time (run, run_host)")

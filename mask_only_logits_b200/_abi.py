@@ -60,6 +60,29 @@ PROTOTYPES = {
                             ctypes.POINTER(_i32)]),
 }
 
+class LogitRulesStruct(ctypes.Structure):
+    """dllm_logit_rules (include/dllm.h)."""
+    _fields_ = [("bias", _p), ("bias_stride", ctypes.c_int64), ("counts", _p),
+                ("counts_stride", ctypes.c_int64), ("seen", _p), ("seen_stride", ctypes.c_int64),
+                ("repetition", _p), ("presence", _p), ("frequency", _p), ("allow", _p),
+                ("allow_stride", ctypes.c_int64), ("allow_id", _p), ("allow_rows", _i32)]
+
+
+PROTOTYPES.update({
+    "dllm_masked_logits_rules": (_st, [_p, _p, _p, _i32, _i32, _i32, _i32, _p, _p,
+                                       ctypes.POINTER(LogitRulesStruct), ctypes.c_uint32, _p, _p,
+                                       _p, _p, _p, _p, _p, _p, _p, _sz, _p]),
+    "dllm_token_counts": (_st, [_p, _p, _p, _i32, _i32, _i32, _i32, _p, _p, _p]),
+    "dllm_mx4_scale_bytes": (_sz, [ctypes.c_int64, _i32]),
+    "dllm_mx4_quantize": (_st, [_p, _i32, ctypes.c_int64, _i32, ctypes.c_int64, _p, _p, _p]),
+    "dllm_mx4_dequantize": (_st, [_p, _p, ctypes.c_int64, _i32, _i32, _p, ctypes.c_int64, _p]),
+    "dllm_workspace_bytes_mx4": (_sz, [_i32, _i32, _i32, _i32, ctypes.c_int64]),
+    "dllm_workspace_rows_mx4": (ctypes.c_int64, [_i32, _i32, _i32, _i32, _sz]),
+    "dllm_masked_logits_mx4": (_st, [_p, _p, _p, _p, _i32, _i32, _i32, _i32, _p, _p,
+                                     ctypes.POINTER(LogitRulesStruct), ctypes.c_uint32, _p, _p,
+                                     _p, _p, _p, _p, _p, _p, _p, _sz, _p]),
+})
+
 _lib = None
 
 

@@ -21,6 +21,9 @@
 #include "merge.cuh"
 #include "select.cuh"
 #include "arena.cuh"
+#include "mx4.cuh"
+#include "rules.cuh"
+#include "shaped.cuh"
 
 #ifndef DLLM_GATHER_HOST_CTAS
 #define DLLM_GATHER_HOST_CTAS 1   // gather CTAs per SM when the rows come from host memory
@@ -136,7 +139,8 @@ dllm_status device_state(DeviceState** out) {
            cudaFuncSetAttribute(lm::lmhead_kernel<2, lm::kModeDebugStore>, smem_attr, lm::Cfg<2>::SMEM_BYTES) ||
            cudaFuncSetAttribute(lm::lmhead_auto_kernel<lm::kModeStats>, smem_attr, lm::kAutoSmemBytes) ||
            cudaFuncSetAttribute(lm::lmhead_auto_kernel<lm::kModeStatsExt>, smem_attr, lm::kAutoSmemBytes) ||
-           cudaFuncSetAttribute(lm::lmhead_auto_kernel<lm::kModeDebugStore>, smem_attr, lm::kAutoSmemBytes)))
+           cudaFuncSetAttribute(lm::lmhead_auto_kernel<lm::kModeDebugStore>, smem_attr, lm::kAutoSmemBytes) ||
+           cudaFuncSetAttribute(rules::token_count_kernel, smem_attr, rules::kCountMaxSlice * 4)))
         st.err = DLLM_ERR_CUDA;
       if (st.err == DLLM_OK) {
         // how many CTA pairs of the paired GEMM can be resident at once (a persistent grid
@@ -175,15 +179,16 @@ dllm_status device_state(DeviceState** out) {
 }
 
 // Workspace layout for at most `rows` masked rows (rows = B*L: any mask):
-// [tile counts | unit counters | gathered rows Hm | part_m | part_s | part_a | part_t | part_m2].
+// [tile counts | unit counters | gathered rows Hm | part_m | part_s | part_a | part_t | part_m2];
+// with MXFP4 operands Hm holds the rows' codes, and their scales (hs_off) follow it.
 struct WsLayout {
-  size_t tiles_off, ctr_off, hm_off, pm_off, ps_off, pa_off, pt_off, pm2_off, total;
+  size_t tiles_off, ctr_off, hm_off, hs_off, pm_off, ps_off, pa_off, pt_off, pm2_off, total;
   long long part_cap;
   long long rows;          // masked-row capacity: rows of Hm, and the GEMM's row bound
   int n_ctr;
 };
 
-WsLayout ws_layout(int B, int L, int d, int V, long long rows) {
+WsLayout ws_layout(int B, int L, int d, int V, long long rows, bool mx4 = false) {
   WsLayout w{};
   const long long n = static_cast<long long>(B) * L;
   const long long ntiles = (n + kCompactTile - 1) / kCompactTile;
@@ -215,7 +220,9 @@ WsLayout ws_layout(int B, int L, int d, int V, long long rows) {
   size_t off = 0;
   w.tiles_off = off; off = round_up(off + sizeof(int) * ntiles, 256);
   w.ctr_off = off;   off = round_up(off + sizeof(int) * static_cast<size_t>(w.n_ctr), 256);
-  w.hm_off = off;    off = round_up(off + static_cast<size_t>(rows) * d * 2, 256);
+  w.hm_off = off;    off = round_up(off + (mx4 ? static_cast<size_t>(rows) * d / 2
+                                               : static_cast<size_t>(rows) * d * 2), 256);
+  w.hs_off = off;    if (mx4) off = round_up(off + static_cast<size_t>(mx4::scale_bytes(rows, d)), 256);
   w.pm_off = off;    off = round_up(off + sizeof(float) * cap, 256);
   w.ps_off = off;    off = round_up(off + sizeof(float) * cap, 256);
   w.pa_off = off;    off = round_up(off + sizeof(int) * cap, 256);
@@ -228,11 +235,11 @@ WsLayout ws_layout(int B, int L, int d, int V, long long rows) {
 // The layout a workspace of ws_bytes can hold: all B*L rows when it is at least the full
 // layout, else the largest masked-row capacity whose layout fits (the total grows with the
 // capacity), or rows = 0 when not even one row fits.
-WsLayout ws_layout_for(int B, int L, int d, int V, size_t ws_bytes) {
+WsLayout ws_layout_for(int B, int L, int d, int V, size_t ws_bytes, bool mx4 = false) {
   const long long n = static_cast<long long>(B) * L;
-  WsLayout full = ws_layout(B, L, d, V, n);
+  WsLayout full = ws_layout(B, L, d, V, n, mx4);
   if (ws_bytes >= full.total) return full;
-  WsLayout one = ws_layout(B, L, d, V, 1);
+  WsLayout one = ws_layout(B, L, d, V, 1, mx4);
   if (ws_bytes < one.total) {
     one.rows = 0;
     return one;
@@ -240,10 +247,10 @@ WsLayout ws_layout_for(int B, int L, int d, int V, size_t ws_bytes) {
   long long lo = 1, hi = n;                   // layout(lo) fits, layout(hi) does not
   while (hi - lo > 1) {
     const long long mid = lo + (hi - lo) / 2;
-    if (ws_layout(B, L, d, V, mid).total <= ws_bytes) lo = mid;
+    if (ws_layout(B, L, d, V, mid, mx4).total <= ws_bytes) lo = mid;
     else hi = mid;
   }
-  return ws_layout(B, L, d, V, lo);
+  return ws_layout(B, L, d, V, lo, mx4);
 }
 
 // A step input (H or M) may live in device memory or in page-locked host memory that the
@@ -503,6 +510,120 @@ dllm_status run_logits(const LogitsArgs& a, bool debug, bool skip_prepare = fals
     g_prof.gemm_launches++;
   }
   return cudaPeekAtLastError() == cudaSuccess ? DLLM_OK : DLLM_ERR_CUDA;
+}
+
+// ---------------------------------------------------------------------------------------
+// Rules on the logits, and MXFP4 operands (dllm_masked_logits_rules, dllm_masked_logits_mx4)
+// ---------------------------------------------------------------------------------------
+bool logits_shape_ok(int B, int L, int d, int V) {
+  return shapes_ok(B, L) && V >= 1 && d >= DLLM_D_MULTIPLE && d % DLLM_D_MULTIPLE == 0;
+}
+
+dllm_status validate_rules(const dllm_logit_rules& r, int B, int V) {
+  const long long words = (static_cast<long long>(V) + 31) / 32;
+  if ((r.counts == nullptr) != (r.seen == nullptr)) return DLLM_ERR_NULL;
+  if (!r.counts && (r.repetition || r.presence || r.frequency)) return DLLM_ERR_NULL;
+  if (r.allow_id && !r.allow) return DLLM_ERR_NULL;
+  const void* ptrs[] = {r.bias, r.counts, r.seen, r.repetition, r.presence, r.frequency, r.allow, r.allow_id};
+  for (const void* p : ptrs)
+    if (p && !aligned16(p)) return DLLM_ERR_ALIGN;
+  if (r.bias && r.bias_stride != 0 && (r.bias_stride < V || r.bias_stride % 4 != 0)) return DLLM_ERR_SHAPE;
+  if (r.counts && (r.counts_stride < V || r.seen_stride < words)) return DLLM_ERR_SHAPE;
+  if (r.allow && (r.allow_stride < words || r.allow_rows < 1)) return DLLM_ERR_SHAPE;
+  if (r.allow && !r.allow_id && r.allow_rows != 1 && r.allow_rows != B) return DLLM_ERR_SHAPE;
+  return DLLM_OK;
+}
+
+struct ShapedArgs {
+  LogitsArgs a;                                  // a.W is null with MXFP4 operands
+  const uint8_t* Wq; const uint8_t* Ws;          // MXFP4 codes and scales of W, or both null
+  const dllm_logit_rules* rules;                 // null: no rules (MXFP4 only)
+};
+
+dllm_status run_shaped(const ShapedArgs& x) {
+  const LogitsArgs& a = x.a;
+  const bool mx4 = x.Wq != nullptr;
+  if (!a.H || !a.M || !a.row_idx || !a.seq_off || !a.count || !a.ws || !a.tok || !a.conf || !a.lse)
+    return DLLM_ERR_NULL;
+  if ((a.win_lo == nullptr) != (a.win_hi == nullptr)) return DLLM_ERR_NULL;
+  if ((a.stats & ~(DLLM_STAT_ENTROPY | DLLM_STAT_MARGIN)) != 0) return DLLM_ERR_SHAPE;
+  if (((a.stats & DLLM_STAT_ENTROPY) != 0) != (a.entropy != nullptr)) return DLLM_ERR_NULL;
+  if (((a.stats & DLLM_STAT_MARGIN) != 0) != (a.margin != nullptr)) return DLLM_ERR_NULL;
+  if (!logits_shape_ok(a.B, a.L, a.d, a.V)) return DLLM_ERR_SHAPE;
+  const void* ptrs[] = {a.H, a.M, a.W, x.Wq, x.Ws, a.row_idx, a.seq_off, a.count, a.ws, a.tok, a.conf,
+                        a.lse, a.entropy, a.margin, a.win_lo, a.win_hi};
+  for (const void* p : ptrs)
+    if (p && !aligned16(p)) return DLLM_ERR_ALIGN;
+  dllm_status st = DLLM_OK;
+  if (x.rules && (st = validate_rules(*x.rules, a.B, a.V)) != DLLM_OK) return st;
+  const WsLayout w = ws_layout_for(a.B, a.L, a.d, a.V, a.ws_bytes, mx4);
+  if (w.rows < 1) return DLLM_ERR_WORKSPACE;
+  DeviceState* ds = nullptr;
+  if ((st = device_state(&ds)) != DLLM_OK) return st;
+  uint8_t* ws = static_cast<uint8_t*>(a.ws);
+  if (!mx4) {
+    if ((st = prepare_rows(a, *ds, w)) != DLLM_OK) return st;
+  } else {
+    const void* Hd = nullptr;
+    const void* Md = nullptr;
+    bool host_rows = false;
+    if ((st = resolve_input(a.H, &Hd, &host_rows)) != DLLM_OK) return st;
+    if ((st = resolve_input(a.M, &Md)) != DLLM_OK) return st;
+    if ((st = launch_compact(static_cast<const uint8_t*>(Md), a.B, a.L, a.win_lo, a.win_hi, a.row_idx,
+                             a.seq_off, a.count, reinterpret_cast<int*>(ws + w.tiles_off), ds->status,
+                             a.s)) != DLLM_OK)
+      return st;
+    if (launch_pdl(mx4::gather_quantize_kernel, dim3(ds->sms * (host_rows ? DLLM_GATHER_HOST_CTAS : 4)),
+                   dim3(mx4::kThreads), 0, a.s, static_cast<const uint16_t*>(Hd), (const int*)a.row_idx,
+                   (const int*)a.count, static_cast<long long>(a.B) * a.L, w.rows, a.d, ws + w.hm_off,
+                   reinterpret_cast<uint32_t*>(ws + w.hs_off), reinterpret_cast<int*>(ws + w.ctr_off),
+                   w.n_ctr, ds->status) != cudaSuccess)
+      return DLLM_ERR_CUDA;
+    count_launch();
+  }
+  const lm::Partials part{reinterpret_cast<float*>(ws + w.pm_off), reinterpret_cast<float*>(ws + w.ps_off),
+                          reinterpret_cast<int*>(ws + w.pa_off), reinterpret_cast<float*>(ws + w.pt_off),
+                          reinterpret_cast<float*>(ws + w.pm2_off)};
+  const lm::Outputs outs{a.tok, a.conf, a.lse, a.entropy, a.margin, a.raw, 0};
+  const dllm_logit_rules rules = x.rules ? *x.rules : dllm_logit_rules{};
+  const int n_cap = static_cast<int>(w.rows);
+  long long n_split = w.part_cap / n_cap;
+  n_split = n_split > 64 ? 64 : n_split;
+  if (n_split < 1) return DLLM_ERR_WORKSPACE;
+  const shaped::Operands o{reinterpret_cast<uint16_t*>(ws + w.hm_off), a.W, ws + w.hm_off, ws + w.hs_off,
+                           x.Wq, x.Ws};
+  const dim3 grid((n_cap + shaped::BM - 1) / shaped::BM, static_cast<unsigned>(n_split));
+#define DLLM_LAUNCH_SHAPED(MX4, EXT)                                                             \
+  launch_pdl(shaped::shaped_kernel<MX4, EXT>, grid, dim3(shaped::kThreads), 0, a.s, o,            \
+             (const int*)a.count, n_cap, a.V, a.d, a.L, rules, (const int*)a.row_idx, part,       \
+             static_cast<int>(n_split), ds->status)
+  cudaError_t e = mx4 ? (a.stats ? DLLM_LAUNCH_SHAPED(true, true) : DLLM_LAUNCH_SHAPED(true, false))
+                      : (a.stats ? DLLM_LAUNCH_SHAPED(false, true) : DLLM_LAUNCH_SHAPED(false, false));
+#undef DLLM_LAUNCH_SHAPED
+  if (e != cudaSuccess) return DLLM_ERR_CUDA;
+  e = a.stats ? launch_pdl(shaped::shaped_merge_kernel<true>, dim3(ds->sms), dim3(shaped::kThreads), 0, a.s,
+                           part, (const int*)a.count, n_cap, static_cast<int>(n_split), outs)
+              : launch_pdl(shaped::shaped_merge_kernel<false>, dim3(ds->sms), dim3(shaped::kThreads), 0, a.s,
+                           part, (const int*)a.count, n_cap, static_cast<int>(n_split), outs);
+  if (e != cudaSuccess) return DLLM_ERR_CUDA;
+  count_launch(2);
+  return DLLM_OK;
+}
+
+dllm_status mx4_checks(const void* X, int dtype, bool f16_ok, int64_t rows, int32_t cols, int64_t ld,
+                       const void* q, const void* s) {
+  if (!X || !q || !s) return DLLM_ERR_NULL;
+  if (rows < 1 || rows >= (1ll << 31) || cols < 32 || cols % 32 != 0 || ld < cols) return DLLM_ERR_SHAPE;
+  if (dtype != DLLM_BF16 && dtype != DLLM_F32 && !(f16_ok && dtype == DLLM_F16)) return DLLM_ERR_SHAPE;
+  if (!aligned16(X) || !aligned16(q) || !aligned16(s) || ld % (dtype == DLLM_F32 ? 4 : 8) != 0)
+    return DLLM_ERR_ALIGN;
+  return DLLM_OK;
+}
+
+// Blocks of a grid-stride kernel: one per `per` items, at most `most`.
+unsigned grid_for(long long items, int per, long long most) {
+  const long long g = (items + per - 1) / per;
+  return static_cast<unsigned>(g < 1 ? 1 : (g > most ? most : g));
 }
 
 }  // namespace
@@ -915,6 +1036,126 @@ dllm_status dllm_prof_end(double* gemm_ms, int32_t* gemm_launches, int32_t* kern
   g_prof.on = false;
   g_prof.used = 0;
   return st;
+}
+
+dllm_status dllm_masked_logits_rules(const uint16_t* H, const uint8_t* M, const uint16_t* W, int32_t B,
+                                     int32_t L, int32_t d, int32_t V, const int32_t* win_lo,
+                                     const int32_t* win_hi, const dllm_logit_rules* rules, uint32_t stats,
+                                     int32_t* tok, float* conf, float* lse, float* entropy, float* margin,
+                                     int32_t* row_idx, int32_t* seq_off, int32_t* count, void* ws,
+                                     size_t ws_bytes, void* stream) {
+  const dllm::NvtxRange nvtx_range("dllm_masked_logits_rules");
+  if (!W || !rules) return DLLM_ERR_NULL;
+  ShapedArgs x{{H, M, W, B, L, d, V, win_lo, win_hi, stats, entropy, margin, tok, conf, lse, nullptr,
+                row_idx, seq_off, count, ws, ws_bytes, static_cast<cudaStream_t>(stream)},
+               nullptr, nullptr, rules};
+  return run_shaped(x);
+}
+
+dllm_status dllm_token_counts(const int32_t* tokens, const uint8_t* M, const int32_t* n_valid, int32_t B,
+                              int32_t n, int32_t V, int32_t accumulate, int32_t* counts, uint32_t* seen,
+                              void* stream) {
+  const dllm::NvtxRange nvtx_range("dllm_token_counts");
+  if ((!tokens && n != 0) || !counts || !seen) return DLLM_ERR_NULL;
+  if (B < 1 || B > 65535 || n < 0 || V < 1 || (accumulate != 0 && accumulate != 1)) return DLLM_ERR_SHAPE;
+  const void* ptrs[] = {tokens, M, n_valid, counts, seen};
+  for (const void* p : ptrs)
+    if (p && !aligned16(p)) return DLLM_ERR_ALIGN;
+  if (accumulate && n == 0) return DLLM_OK;
+  DeviceState* ds = nullptr;
+  dllm_status st = device_state(&ds);
+  if (st != DLLM_OK) return st;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (accumulate) {
+    if (launch_pdl(rules::token_add_kernel, dim3(grid_for(n, rules::kCountThreads, ds->sms), B),
+                   dim3(rules::kCountThreads), 0, s, tokens, M, n_valid, n, V, counts, seen) != cudaSuccess)
+      return DLLM_ERR_CUDA;
+  } else {
+    // slices of the vocabulary: enough CTAs for every SM, at most what shared memory holds
+    const long long per_seq = B < ds->sms ? ds->sms / B : 1;
+    long long slice = ((V + per_seq - 1) / per_seq + 31) / 32 * 32;
+    if (slice > rules::kCountMaxSlice) slice = rules::kCountMaxSlice;
+    if (launch_pdl(rules::token_count_kernel, dim3(grid_for(V, static_cast<int>(slice), 1ll << 30), B),
+                   dim3(rules::kCountThreads), static_cast<size_t>(slice) * 4, s, tokens, M, n_valid, n, V,
+                   static_cast<int>(slice), counts, seen) != cudaSuccess)
+      return DLLM_ERR_CUDA;
+  }
+  count_launch();
+  return DLLM_OK;
+}
+
+size_t dllm_mx4_scale_bytes(int64_t rows, int32_t cols) {
+  if (rows < 1 || rows >= (1ll << 31) || cols < 32 || cols % 32 != 0) return 0;
+  return static_cast<size_t>(mx4::scale_bytes(rows, cols));
+}
+
+dllm_status dllm_mx4_quantize(const void* X, int32_t dtype, int64_t rows, int32_t cols, int64_t ld,
+                              uint8_t* q, uint8_t* s, void* stream) {
+  const dllm::NvtxRange nvtx_range("dllm_mx4_quantize");
+  dllm_status st = mx4_checks(X, dtype, true, rows, cols, ld, q, s);
+  if (st != DLLM_OK) return st;
+  DeviceState* ds = nullptr;
+  if ((st = device_state(&ds)) != DLLM_OK) return st;
+  const long long blocks = (rows + 127) / 128 * 128 * ((cols + 127) / 128 * 4);
+  const dim3 grid(grid_for(blocks, mx4::kThreads, ds->sms * 16ll)), thr(mx4::kThreads);
+  uint32_t* sw = reinterpret_cast<uint32_t*>(s);
+  const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (dtype == DLLM_BF16)
+    e = launch_pdl(mx4::quantize_kernel<__nv_bfloat16>, grid, thr, 0, cs, static_cast<const __nv_bfloat16*>(X),
+                   (long long)rows, cols, (long long)ld, q, sw);
+  else if (dtype == DLLM_F16)
+    e = launch_pdl(mx4::quantize_kernel<__half>, grid, thr, 0, cs, static_cast<const __half*>(X),
+                   (long long)rows, cols, (long long)ld, q, sw);
+  else
+    e = launch_pdl(mx4::quantize_kernel<float>, grid, thr, 0, cs, static_cast<const float*>(X),
+                   (long long)rows, cols, (long long)ld, q, sw);
+  if (e != cudaSuccess) return DLLM_ERR_CUDA;
+  count_launch();
+  return DLLM_OK;
+}
+
+dllm_status dllm_mx4_dequantize(const uint8_t* q, const uint8_t* s, int64_t rows, int32_t cols, int32_t dtype,
+                                void* X, int64_t ld, void* stream) {
+  const dllm::NvtxRange nvtx_range("dllm_mx4_dequantize");
+  dllm_status st = mx4_checks(X, dtype, false, rows, cols, ld, q, s);
+  if (st != DLLM_OK) return st;
+  DeviceState* ds = nullptr;
+  if ((st = device_state(&ds)) != DLLM_OK) return st;
+  const dim3 grid(grid_for(rows * (cols / 8), mx4::kThreads, ds->sms * 16ll)), thr(mx4::kThreads);
+  const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = dtype == DLLM_BF16
+      ? launch_pdl(mx4::dequantize_kernel<__nv_bfloat16>, grid, thr, 0, cs, q, s, (long long)rows, cols,
+                   static_cast<__nv_bfloat16*>(X), (long long)ld)
+      : launch_pdl(mx4::dequantize_kernel<float>, grid, thr, 0, cs, q, s, (long long)rows, cols,
+                   static_cast<float*>(X), (long long)ld);
+  if (e != cudaSuccess) return DLLM_ERR_CUDA;
+  count_launch();
+  return DLLM_OK;
+}
+
+size_t dllm_workspace_bytes_mx4(int32_t B, int32_t L, int32_t d, int32_t V, int64_t max_rows) {
+  if (!logits_shape_ok(B, L, d, V) || max_rows < 1) return 0;
+  return ws_layout(B, L, d, V, max_rows, true).total;
+}
+
+int64_t dllm_workspace_rows_mx4(int32_t B, int32_t L, int32_t d, int32_t V, size_t ws_bytes) {
+  if (!logits_shape_ok(B, L, d, V)) return 0;
+  return ws_layout_for(B, L, d, V, ws_bytes, true).rows;
+}
+
+dllm_status dllm_masked_logits_mx4(const uint16_t* H, const uint8_t* M, const uint8_t* Wq, const uint8_t* Ws,
+                                   int32_t B, int32_t L, int32_t d, int32_t V, const int32_t* win_lo,
+                                   const int32_t* win_hi, const dllm_logit_rules* rules, uint32_t stats,
+                                   int32_t* tok, float* conf, float* lse, float* entropy, float* margin,
+                                   int32_t* row_idx, int32_t* seq_off, int32_t* count, void* ws,
+                                   size_t ws_bytes, void* stream) {
+  const dllm::NvtxRange nvtx_range("dllm_masked_logits_mx4");
+  if (!Wq || !Ws) return DLLM_ERR_NULL;
+  ShapedArgs x{{H, M, nullptr, B, L, d, V, win_lo, win_hi, stats, entropy, margin, tok, conf, lse, nullptr,
+                row_idx, seq_off, count, ws, ws_bytes, static_cast<cudaStream_t>(stream)},
+               Wq, Ws, rules};
+  return run_shaped(x);
 }
 
 }  // extern "C"

@@ -467,7 +467,7 @@ dllm_status dllm_decode_block_step(const uint16_t* H, const uint8_t* M, const ui
  *                  - presence[b] - frequency[b] * c                  : z0
  *     z2 = z1 + bias[b, v]
  *     z  = allowed ? z2 : -infinity
- * and tok, lse, conf and the scores are those of z (fp32, one rounding per step).  Every
+ * and tok, lse, conf and the scores are those of z (evaluated in fp32).  Every
  * pointer may be NULL: without counts no penalty applies, a NULL penalty is neutral
  * (repetition 1, presence 0, frequency 0).  The struct is read during the call; what its
  * pointers name is read by the kernels.

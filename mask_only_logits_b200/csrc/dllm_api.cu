@@ -140,6 +140,12 @@ dllm_status device_state(DeviceState** out) {
            cudaFuncSetAttribute(lm::lmhead_auto_kernel<lm::kModeStats>, smem_attr, lm::kAutoSmemBytes) ||
            cudaFuncSetAttribute(lm::lmhead_auto_kernel<lm::kModeStatsExt>, smem_attr, lm::kAutoSmemBytes) ||
            cudaFuncSetAttribute(lm::lmhead_auto_kernel<lm::kModeDebugStore>, smem_attr, lm::kAutoSmemBytes) ||
+           cudaFuncSetAttribute(shaped::shaped_kernel<shaped::Bf16, true, false>, smem_attr, shaped::smem_bytes<shaped::Bf16>()) ||
+           cudaFuncSetAttribute(shaped::shaped_kernel<shaped::Bf16, true, true>, smem_attr, shaped::smem_bytes<shaped::Bf16>()) ||
+           cudaFuncSetAttribute(shaped::shaped_kernel<shaped::Mx4, true, false>, smem_attr, shaped::smem_bytes<shaped::Mx4>()) ||
+           cudaFuncSetAttribute(shaped::shaped_kernel<shaped::Mx4, true, true>, smem_attr, shaped::smem_bytes<shaped::Mx4>()) ||
+           cudaFuncSetAttribute(shaped::shaped_kernel<shaped::Mx4, false, false>, smem_attr, shaped::smem_bytes<shaped::Mx4>()) ||
+           cudaFuncSetAttribute(shaped::shaped_kernel<shaped::Mx4, false, true>, smem_attr, shaped::smem_bytes<shaped::Mx4>()) ||
            cudaFuncSetAttribute(rules::token_count_kernel, smem_attr, rules::kCountMaxSlice * 4)))
         st.err = DLLM_ERR_CUDA;
       if (st.err == DLLM_OK) {
@@ -540,6 +546,90 @@ struct ShapedArgs {
   const dllm_logit_rules* rules;                 // null: no rules (MXFP4 only)
 };
 
+// A 2-D map of rows of `cols` elements (row pitch cols * bytes), boxes of box_cols x box_rows.
+dllm_status make_map(CUtensorMap* tm, CUtensorMapDataType type, int bytes, const void* base, uint64_t rows,
+                     uint64_t cols, uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swizzle) {
+  const cuuint64_t dims[2] = {cols, rows};
+  const cuuint64_t strides[1] = {cols * bytes};
+  const cuuint32_t box[2] = {box_cols, box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r = g_encode(tm, type, 2, const_cast<void*>(base), dims, strides, box, estr,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? DLLM_OK : DLLM_ERR_CUDA;
+}
+
+// The GEMM on prepared rows: one launch in clusters of two CTAs.
+template <class Op>
+dllm_status launch_shaped(const ShapedArgs& x, const DeviceState& ds, const WsLayout& w,
+                          const lm::Partials& part, const lm::Outputs& outs) {
+  const LogitsArgs& a = x.a;
+  if (ds.pairs < 1) return DLLM_ERR_DEVICE;
+  uint8_t* ws = static_cast<uint8_t*>(a.ws);
+  const void* Hm = ws + w.hm_off;
+  const uint64_t n = static_cast<uint64_t>(w.rows), V = static_cast<uint64_t>(a.V);
+  CUtensorMap tmA1, tmA2, tmB1, tmB2, tmSA, tmSB;
+  const auto sw128 = CU_TENSOR_MAP_SWIZZLE_128B;
+  dllm_status st = DLLM_OK;
+  auto map = [&](CUtensorMap* tm, const void* base, uint64_t rows, uint32_t box_rows) {
+    if (st != DLLM_OK) return;
+    st = Op::kMx4 ? make_map(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, base, rows, a.d / 2, 128, box_rows, sw128)
+                  : make_map(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, rows, a.d, 64, box_rows, sw128);
+  };
+  const void* W = Op::kMx4 ? static_cast<const void*>(x.Wq) : static_cast<const void*>(a.W);
+  map(&tmA1, Hm, n, 32);
+  map(&tmA2, Hm, n, 128);
+  map(&tmB1, W, V, Op::BN);
+  map(&tmB2, W, V, Op::BN / 2);
+  if (Op::kMx4 && st == DLLM_OK) {
+    // scale tiles as rows of ceil(d / 128) * 512 bytes, in 8-byte words: 1024 bytes a stage
+    const uint64_t words = static_cast<uint64_t>((a.d + 127) / 128) * 64;
+    st = make_map(&tmSA, CU_TENSOR_MAP_DATA_TYPE_UINT64, 8, ws + w.hs_off, (n + 127) / 128, words, 128, 1,
+                  CU_TENSOR_MAP_SWIZZLE_NONE);
+    if (st == DLLM_OK)
+      st = make_map(&tmSB, CU_TENSOR_MAP_DATA_TYPE_UINT64, 8, x.Ws, (V + 127) / 128, words, 128, 2,
+                    CU_TENSOR_MAP_SWIZZLE_NONE);
+  } else {
+    tmSA = tmSB = tmA1;                                                // not used
+  }
+  if (st != DLLM_OK) return st;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  cfg.gridDim = dim3(2 * ds.pairs, 1, 1);
+  cfg.blockDim = dim3(shaped::kThreads, 1, 1);
+  cfg.dynamicSmemBytes = shaped::smem_bytes<Op>();
+  cfg.stream = a.s;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  const shaped::Problem p{static_cast<int>(w.rows), a.V, a.d, a.L, a.row_idx, part, w.part_cap,
+                          reinterpret_cast<int*>(ws + w.ctr_off), outs, ds.status};
+  const dllm_logit_rules rules = x.rules ? *x.rules : dllm_logit_rules{};
+  const int* count = a.count;
+  const int variant = g_gemm_variant.load();
+#define DLLM_LAUNCH_SHAPED(RULES, EXT)                                                            \
+  cudaLaunchKernelEx(&cfg, shaped::shaped_kernel<Op, RULES, EXT>, tmA1, tmA2, tmB1, tmB2, tmSA,    \
+                     tmSB, count, variant, p, rules)
+  cudaError_t e;
+  if constexpr (Op::kMx4) {
+    if (!x.rules)
+      e = a.stats ? DLLM_LAUNCH_SHAPED(false, true) : DLLM_LAUNCH_SHAPED(false, false);
+    else
+      e = a.stats ? DLLM_LAUNCH_SHAPED(true, true) : DLLM_LAUNCH_SHAPED(true, false);
+  } else {
+    e = a.stats ? DLLM_LAUNCH_SHAPED(true, true) : DLLM_LAUNCH_SHAPED(true, false);
+  }
+#undef DLLM_LAUNCH_SHAPED
+  if (e != cudaSuccess) return DLLM_ERR_CUDA;
+  count_launch();
+  return cudaPeekAtLastError() == cudaSuccess ? DLLM_OK : DLLM_ERR_CUDA;
+}
+
 dllm_status run_shaped(const ShapedArgs& x) {
   const LogitsArgs& a = x.a;
   const bool mx4 = x.Wq != nullptr;
@@ -585,29 +675,7 @@ dllm_status run_shaped(const ShapedArgs& x) {
                           reinterpret_cast<int*>(ws + w.pa_off), reinterpret_cast<float*>(ws + w.pt_off),
                           reinterpret_cast<float*>(ws + w.pm2_off)};
   const lm::Outputs outs{a.tok, a.conf, a.lse, a.entropy, a.margin, a.raw, 0};
-  const dllm_logit_rules rules = x.rules ? *x.rules : dllm_logit_rules{};
-  const int n_cap = static_cast<int>(w.rows);
-  long long n_split = w.part_cap / n_cap;
-  n_split = n_split > 64 ? 64 : n_split;
-  if (n_split < 1) return DLLM_ERR_WORKSPACE;
-  const shaped::Operands o{reinterpret_cast<uint16_t*>(ws + w.hm_off), a.W, ws + w.hm_off, ws + w.hs_off,
-                           x.Wq, x.Ws};
-  const dim3 grid((n_cap + shaped::BM - 1) / shaped::BM, static_cast<unsigned>(n_split));
-#define DLLM_LAUNCH_SHAPED(MX4, EXT)                                                             \
-  launch_pdl(shaped::shaped_kernel<MX4, EXT>, grid, dim3(shaped::kThreads), 0, a.s, o,            \
-             (const int*)a.count, n_cap, a.V, a.d, a.L, rules, (const int*)a.row_idx, part,       \
-             static_cast<int>(n_split), ds->status)
-  cudaError_t e = mx4 ? (a.stats ? DLLM_LAUNCH_SHAPED(true, true) : DLLM_LAUNCH_SHAPED(true, false))
-                      : (a.stats ? DLLM_LAUNCH_SHAPED(false, true) : DLLM_LAUNCH_SHAPED(false, false));
-#undef DLLM_LAUNCH_SHAPED
-  if (e != cudaSuccess) return DLLM_ERR_CUDA;
-  e = a.stats ? launch_pdl(shaped::shaped_merge_kernel<true>, dim3(ds->sms), dim3(shaped::kThreads), 0, a.s,
-                           part, (const int*)a.count, n_cap, static_cast<int>(n_split), outs)
-              : launch_pdl(shaped::shaped_merge_kernel<false>, dim3(ds->sms), dim3(shaped::kThreads), 0, a.s,
-                           part, (const int*)a.count, n_cap, static_cast<int>(n_split), outs);
-  if (e != cudaSuccess) return DLLM_ERR_CUDA;
-  count_launch(2);
-  return DLLM_OK;
+  return mx4 ? launch_shaped<shaped::Mx4>(x, *ds, w, part, outs) : launch_shaped<shaped::Bf16>(x, *ds, w, part, outs);
 }
 
 dllm_status mx4_checks(const void* X, int dtype, bool f16_ok, int64_t rows, int32_t cols, int64_t ld,

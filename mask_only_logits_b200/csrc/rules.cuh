@@ -7,8 +7,7 @@
 //   z2 = z1 + bias[b, v]
 //   z  = allowed(row, v) ? z2 : -inf
 // The rules act on the accumulator chunk of 32 columns that the LM head's epilogue holds in
-// registers, so a shaped logit is never stored either.  Every step is rounded to fp32 on its
-// own (no contraction), the same as the formula evaluated step by step in fp32.
+// registers, so a shaped logit is never stored either; they are evaluated in fp32.
 //
 // The row states here differ from lmhead.cuh's in what rules make possible: a row, a split or
 // a chunk with nothing allowed (max = -inf), and logits at the lowest finite value (a bias of
@@ -28,11 +27,11 @@ struct RowRules {
   const int* counts;
   const uint32_t* seen;
   const uint32_t* allow;
-  float theta, presence, frequency;
+  float theta, inverse, presence, frequency;     // inverse = 1 / theta
 };
 
 __device__ __forceinline__ RowRules no_rules() {
-  return RowRules{nullptr, nullptr, nullptr, nullptr, 1.f, 0.f, 0.f};
+  return RowRules{nullptr, nullptr, nullptr, nullptr, 1.f, 1.f, 0.f, 0.f};
 }
 
 // The rules of the row at flat position pos (= b * L + l).  A bitmap number past the table is
@@ -45,6 +44,7 @@ __device__ __forceinline__ RowRules row_rules(const dllm_logit_rules& r, int pos
     o.counts = r.counts + b * r.counts_stride;
     o.seen = r.seen + b * r.seen_stride;
     if (r.repetition) o.theta = r.repetition[b];
+    o.inverse = 1.0f / o.theta;
     if (r.presence) o.presence = r.presence[b];
     if (r.frequency) o.frequency = r.frequency[b];
   }
@@ -56,81 +56,165 @@ __device__ __forceinline__ RowRules row_rules(const dllm_logit_rules& r, int pos
   return o;
 }
 
+// theta's reciprocal is rounded once per row: z * inverse is within one unit in the last place
+// of z / theta, and the 32 columns of a chunk stay free of the division's branches (with them
+// a chunk of penalised columns took 5000 cycles).
 __device__ __forceinline__ float penalise(float z, int c, const RowRules& r) {
-  z = z > 0.f ? __fdiv_rn(z, r.theta) : __fmul_rn(z, r.theta);
-  return __fsub_rn(__fsub_rn(z, r.presence), __fmul_rn(r.frequency, static_cast<float>(c)));
+  const float y = __fadd_rn(__fmul_rn(z, z > 0.f ? r.inverse : r.theta), -r.presence);
+  return fmaf(-r.frequency, static_cast<float>(c), y);
 }
 
-// Shape the 32 logits of columns col0 .. col0+31 (col0 a multiple of 32) of each lane's row;
-// columns at and past V become -inf.  Called by all 32 lanes of a warp together: the tests
-// that skip a rule are taken for the warp, whose rows mostly share a sequence.
-__device__ __forceinline__ void shape_chunk(float (&v)[32], int col0, int V, const RowRules& r) {
+// The words of a row's two bitmaps that cover columns col0 .. col0+31 (col0 a multiple of 32;
+// bits at and past V cleared): which of them the sequence holds, and which are allowed.
+struct Words {
+  uint32_t seen, ok;
+};
+__device__ __forceinline__ Words load_words(int col0, int V, const RowRules& r) {
   const int left = V - col0;
   const uint32_t in = left >= 32 ? 0xffffffffu : (left > 0 ? (1u << left) - 1u : 0u);
-  const uint32_t seen = r.seen && in ? __ldg(r.seen + (col0 >> 5)) & in : 0u;
-  const uint32_t ok = r.allow && in ? __ldg(r.allow + (col0 >> 5)) & in : in;
-  const uint32_t any_seen = __reduce_or_sync(0xffffffffu, seen);
-  if (any_seen != 0u) {
-#pragma unroll
-    for (int j = 0; j < 32; ++j)
-      if ((any_seen >> j) & 1u) {
-        if ((seen >> j) & 1u) v[j] = penalise(v[j], __ldg(r.counts + col0 + j), r);
-      }
+  return Words{r.seen && in ? __ldg(r.seen + (col0 >> 5)) & in : 0u,
+               r.allow && in ? __ldg(r.allow + (col0 >> 5)) & in : in};
+}
+
+__device__ __forceinline__ void prefetch_l1(const void* p) {
+  asm volatile("prefetch.global.L1 [%0];" ::"l"(p));
+}
+
+// Ask for the counts and biases that shape_chunk will read for this chunk.
+__device__ __forceinline__ void prefetch_chunk(int col0, int V, const RowRules& r, const Words& w) {
+  if (w.ok == 0u) return;
+  const int last = col0 + 31 < V ? col0 + 31 : V - 1;
+  if (w.seen != 0u) {
+    prefetch_l1(r.counts + col0);
+    prefetch_l1(r.counts + last);
   }
-  if (__any_sync(0xffffffffu, r.bias != nullptr)) {
-    if (r.bias != nullptr) {
-      if (left >= 32) {
+  if (r.bias != nullptr) {
+    prefetch_l1(r.bias + col0);
+    prefetch_l1(r.bias + last);
+  }
+}
+
+// Shape the 32 logits of columns col0 .. col0+31 of each lane's row; what is not allowed, and
+// columns at and past V, become -inf.  Called by all 32 lanes of a warp together: the tests
+// that skip a rule are taken for the warp, whose rows mostly share a sequence.  Returns false
+// if nothing is left in any lane.
+__device__ __forceinline__ bool shape_chunk(float (&v)[32], int col0, int V, const RowRules& r,
+                                            const Words& w) {
+  if (__reduce_or_sync(0xffffffffu, w.ok) == 0u) return false;
+  const uint32_t any_seen = __reduce_or_sync(0xffffffffu, w.seen);
+  if (any_seen != 0u) {
+    // eight columns at a time, without branches: all their counts are asked for before the
+    // first is used
 #pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-          const float4 b = __ldg(reinterpret_cast<const float4*>(r.bias + col0 + j));
-          v[j + 0] = __fadd_rn(v[j + 0], b.x);
-          v[j + 1] = __fadd_rn(v[j + 1], b.y);
-          v[j + 2] = __fadd_rn(v[j + 2], b.z);
-          v[j + 3] = __fadd_rn(v[j + 3], b.w);
-        }
-      } else {
+    for (int g = 0; g < 32; g += 8) {
+      if (((any_seen >> g) & 0xffu) == 0u) continue;
+      int c[8];
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (j < left) v[j] = __fadd_rn(v[j], __ldg(r.bias + col0 + j));
+      for (int j = 0; j < 8; ++j) {
+        c[j] = 0;
+        if ((w.seen >> (g + j)) & 1u) c[j] = __ldg(r.counts + col0 + g + j);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float y = penalise(v[g + j], c[j], r);
+        v[g + j] = (w.seen >> (g + j)) & 1u ? y : v[g + j];
       }
     }
   }
-  if (!__all_sync(0xffffffffu, ok == 0xffffffffu)) {
+  if (r.bias != nullptr) {
+    if (col0 + 32 <= V) {
+#pragma unroll
+      for (int j = 0; j < 32; j += 4) {
+        const float4 b = __ldg(reinterpret_cast<const float4*>(r.bias + col0 + j));
+        v[j + 0] = __fadd_rn(v[j + 0], b.x);
+        v[j + 1] = __fadd_rn(v[j + 1], b.y);
+        v[j + 2] = __fadd_rn(v[j + 2], b.z);
+        v[j + 3] = __fadd_rn(v[j + 3], b.w);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (col0 + j < V) v[j] = __fadd_rn(v[j], __ldg(r.bias + col0 + j));
+    }
+  }
+  if (!__all_sync(0xffffffffu, w.ok == 0xffffffffu)) {
 #pragma unroll
     for (int j = 0; j < 32; ++j)
-      if (!((ok >> j) & 1u)) v[j] = -INFINITY;
+      if (!((w.ok >> j) & 1u)) v[j] = -INFINITY;
   }
+  return true;
+}
+
+// Running statistics of one row, as lm::RowState, with the rounding errors of s and t carried
+// along (Kahan): a row's sum grows by thousands of chunks, each small against it, and adding
+// them plainly lost up to 6e-6 of it.
+struct State {
+  float m, s, t, m2;
+  int a;
+  float sc, tc;                                // what s and t hold too much
+  __device__ __forceinline__ void reset() {
+    m = m2 = -INFINITY;
+    s = t = sc = tc = 0.f;
+    a = 0;
+  }
+  __device__ __forceinline__ lm::RowState value() const {
+    lm::RowState r;
+    r.m = m;
+    r.s = s - sc;
+    r.t = t - tc;
+    r.m2 = m2;
+    r.a = a;
+    return r;
+  }
+};
+
+__device__ __forceinline__ void kahan(float& sum, float& over, float x) {
+  const float y = x - over;
+  const float n = sum + y;
+  over = (n - sum) - y;
+  sum = n;
 }
 
 // Fold 32 logits (columns col0 ..) into a row's state (see above for how this differs from
 // lm::fold_chunk).
 template <bool kExt>
-__device__ __forceinline__ void fold(const float (&v)[32], int col0, lm::RowState& st) {
-  float mx = v[0];
-#pragma unroll
-  for (int j = 1; j < 32; ++j) mx = fmaxf(mx, v[j]);
-  if (mx == -INFINITY) return;                 // nothing allowed in this chunk
-  float c2 = -INFINITY;                        // chunk's second largest (= mx on a tie)
+__device__ __forceinline__ void fold(const float (&v)[32], int col0, State& st) {
+  float mx, c2 = -INFINITY;                    // the chunk's largest and second largest
   if constexpr (kExt) {
-    int n_at_max = 0;
+    float a[4], b[4];
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      n_at_max += v[j] == mx ? 1 : 0;
-      c2 = v[j] == mx ? c2 : fmaxf(c2, v[j]);
+    for (int i = 0; i < 4; ++i) {
+      a[i] = fmaxf(v[2 * i], v[2 * i + 1]);
+      b[i] = fminf(v[2 * i], v[2 * i + 1]);
     }
-    if (n_at_max > 1) c2 = mx;
+#pragma unroll
+    for (int j = 8; j < 32; ++j) {
+      b[j & 3] = fmaxf(b[j & 3], fminf(a[j & 3], v[j]));
+      a[j & 3] = fmaxf(a[j & 3], v[j]);
+    }
+    const float h0 = fmaxf(a[0], a[1]), l0 = fmaxf(fminf(a[0], a[1]), fmaxf(b[0], b[1]));
+    const float h1 = fmaxf(a[2], a[3]), l1 = fmaxf(fminf(a[2], a[3]), fmaxf(b[2], b[3]));
+    mx = fmaxf(h0, h1);
+    c2 = fmaxf(fminf(h0, h1), fmaxf(l0, l1));
+  } else {
+    mx = v[0];
+#pragma unroll
+    for (int j = 1; j < 32; ++j) mx = fmaxf(mx, v[j]);
   }
+  if (mx == -INFINITY) return;                 // nothing allowed in this chunk
   if (mx > st.m) {                             // strict: earlier (lower) index wins ties
     int j0 = 31;
 #pragma unroll
     for (int j = 31; j >= 0; --j)
       if (v[j] == mx) j0 = j;
-    const float sc = ex2_approx((st.m - mx) * lm::kLog2e);
+    const float f = ex2_approx((st.m - mx) * lm::kLog2e);
     if constexpr (kExt) {
-      st.t = sc > 0.f ? sc * (st.t + (st.m - mx) * st.s) : 0.f;
+      st.t = f > 0.f ? f * ((st.t - st.tc) + (st.m - mx) * (st.s - st.sc)) : 0.f;
+      st.tc = 0.f;
       st.m2 = fmaxf(st.m, c2);
     }
-    st.s *= sc;
+    st.s *= f;
+    st.sc *= f;
     st.m = mx;
     st.a = col0 + j0;
   } else if constexpr (kExt) {
@@ -146,37 +230,39 @@ __device__ __forceinline__ void fold(const float (&v)[32], int col0, lm::RowStat
     s1 += e1;
     s2 += e2;
     s3 += e3;
-    if constexpr (kExt) {
-      t0 += e0 > 0.f ? e0 * x0 : 0.f;
-      t1 += e1 > 0.f ? e1 * x1 : 0.f;
-      t0 += e2 > 0.f ? e2 * x2 : 0.f;
-      t1 += e3 > 0.f ? e3 * x3 : 0.f;
+    if constexpr (kExt) {                      // e is 0 long before x reaches the bound
+      t0 = fmaf(e0, fmaxf(x0, -1e4f), t0);
+      t1 = fmaf(e1, fmaxf(x1, -1e4f), t1);
+      t0 = fmaf(e2, fmaxf(x2, -1e4f), t0);
+      t1 = fmaf(e3, fmaxf(x3, -1e4f), t1);
     }
   }
-  st.s += (s0 + s1) + (s2 + s3);
-  if constexpr (kExt) st.t += t0 + t1;
+  kahan(st.s, st.sc, (s0 + s1) + (s2 + s3));
+  if constexpr (kExt) kahan(st.t, st.tc, t0 + t1);
 }
 
-// Merge a later split's state into st (lm::merge_state with the factor guarded).
+// Merge another part of the vocabulary's statistics into st; of equal maxima the lower token
+// wins, so the parts may come in any order.
 template <bool kExt>
 __device__ __forceinline__ void merge(lm::RowState& st, float m, float s, int a, float t, float m2) {
   if (m == -INFINITY) return;
-  if (m > st.m) {                              // strict: the earlier split keeps a tie
-    const float sc = ex2_approx((st.m - m) * lm::kLog2e);
+  if (m > st.m) {
+    const float f = ex2_approx((st.m - m) * lm::kLog2e);
     if constexpr (kExt) {
-      st.t = (sc > 0.f ? sc * (st.t + (st.m - m) * st.s) : 0.f) + t;
+      st.t = (f > 0.f ? f * (st.t + (st.m - m) * st.s) : 0.f) + t;
       st.m2 = fmaxf(st.m, m2);
     }
-    st.s = st.s * sc + s;
+    st.s = st.s * f + s;
     st.m = m;
     st.a = a;
   } else {
-    const float sc = ex2_approx((m - st.m) * lm::kLog2e);
+    const float f = ex2_approx((m - st.m) * lm::kLog2e);
     if constexpr (kExt) {
-      st.t += sc > 0.f ? sc * (t + (m - st.m) * s) : 0.f;
+      st.t += f > 0.f ? f * (t + (m - st.m) * s) : 0.f;
       st.m2 = fmaxf(st.m2, m);
     }
-    st.s += s * sc;
+    st.s += s * f;
+    if (m == st.m && a < st.a) st.a = a;
   }
 }
 

@@ -1,8 +1,28 @@
-// shaped.cuh - the masked LM head with rules on its logits, with bf16 or MXFP4 operands.
+// shaped.cuh - the masked LM head with rules on its logits, with bf16 or MXFP4 operands, on the
+// 5th-generation tensor cores.
 //
-// Plain tiles on the CUDA cores: a CTA owns 64 masked rows and a contiguous range of the
-// vocabulary, forms 64 x 64 logits at a time in registers (fp32), and folds them row by row
-// into the running statistics; shaped_merge_kernel merges the ranges' partials in order.
+// The persistent, warp-specialised structure, the work schedule (Plan) and the split merge are
+// those of lmhead.cuh: per CTA one TMA warp, one MMA warp, and epilogue warps; single CTAs or
+// CTA pairs chosen on the device from the masked count.  What differs:
+//   operands  Bf16: kind::f16, 256 vocabulary columns a tile.
+//             Mx4:  kind::mxf4 with one power-of-two scale per 32 elements of K.  256 elements
+//             of K are 128 bytes, so a stage holds four times the K of a bf16 stage.  The
+//             scales of a stage are copied from shared memory to TMEM (tcgen05.cp, each 512-byte
+//             tile to 4 columns, replicated over the four lane quadrants) ahead of its MMAs.
+//             TMEM holds two accumulators and, per stage of the ring, the stage's scales; with
+//             192 columns a tile that is 2 x 192 + 5 x 24 = 504 of 512 columns.  A stage's
+//             scale columns are rewritten only after the MMAs that read them have released the
+//             stage.  A tile of 192 columns starts on a scale tile (128 rows of W) or in the
+//             middle of one: it takes two scale tiles and, if odd, starts two columns in.
+//   A rows    single CTAs load their rows of Hm in boxes of 32, only as many as are masked.
+//   epilogue  eight warps: two per TMEM lane quadrant, each with half of a tile's columns (the
+//             rules and scores cost more instructions than the plain statistics, and four MXFP4
+//             tiles take the time of one bf16 tile).  rules::shape_chunk on each 32 logits, then
+//             the fold and merge of rules.cuh.  Warps without a masked row only release the
+//             accumulator.  The bitmap words of a tile are loaded, and its counts and biases
+//             asked for, before the wait for its accumulator.
+//   merge     of at most 32 rows: a warp per row, its lanes over the splits (a row's partials
+//             then come in one or two rounds of loads instead of one per eight splits).
 #pragma once
 #include "mx4.cuh"
 #include "rules.cuh"
@@ -10,119 +30,613 @@
 namespace dllm {
 namespace shaped {
 
-constexpr int kThreads = 256;
-constexpr int BM = 64, BN = 64, BK = 32;
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 64 + 32 * kEpiWarps;
+using lm::Outputs;
+using lm::Partials;
+using lm::Plan;
+using lm::RowState;
+using lm::Unit;
 
-struct Operands {
-  const uint16_t* Hm; const uint16_t* W;                       // bf16
-  const uint8_t* Hq; const uint8_t* Hs; const uint8_t* Wq; const uint8_t* Ws;   // MXFP4
+struct Bf16 {
+  static constexpr bool kMx4 = false;
+  static constexpr int BN = 256;        // vocabulary entries per tile
+  static constexpr int BK = 64;         // K per stage: 128 bytes
+  static constexpr int UK = 16;         // K per tcgen05.mma
+  static constexpr int SFA = 0, SFB = 0, kSfCols = 0;
+  static constexpr int kStages1 = 4, kStages2 = 6;
+};
+struct Mx4 {
+  static constexpr bool kMx4 = true;
+  static constexpr int BN = 192;
+  static constexpr int BK = 256;
+  static constexpr int UK = 64;
+  static constexpr int SFA = 1024;      // scale bytes per stage: 128 rows of Hm, 8 blocks
+  static constexpr int SFB = 2048;      // 256 rows of W
+  static constexpr int kSfCols = 24;    // TMEM columns of one stage's scales
+  static constexpr int kStages1 = 5, kStages2 = 5;
 };
 
-template <bool kMx4>
-__device__ __forceinline__ float element(const Operands& o, bool a, long long r, int k, int d) {
-  if constexpr (!kMx4) {
-    const uint16_t b = (a ? o.Hm : o.W)[r * d + k];
-    return __uint_as_float(static_cast<uint32_t>(b) << 16);
+template <int CG, class Op>
+struct Cfg {
+  static constexpr int BM_CTA = 128;                 // rows per CTA (TMEM lanes)
+  static constexpr int BM = BM_CTA * CG;             // rows per m-tile
+  static constexpr int B_ROWS = Op::BN / CG;         // W rows staged per CTA per stage
+  static constexpr int A_BYTES = BM_CTA * 128;
+  static constexpr int B_BYTES = B_ROWS * 128;
+  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + Op::SFA + Op::SFB;
+  static constexpr int kStages = CG == 1 ? Op::kStages1 : Op::kStages2;
+  static constexpr int kCombBytes = 4 * BM_CTA * 20;
+  static constexpr int SMEM_BYTES = 1024 + kStages * STAGE_BYTES + 256 + kCombBytes;
+  static_assert(SMEM_BYTES <= 232448, "exceeds the 227 KB of shared memory of one CTA");
+  static_assert(B_BYTES % 1024 == 0, "B tiles start on swizzle atoms");
+  static_assert(2 * Op::BN + kStages * Op::kSfCols <= 512, "exceeds TMEM");
+  static constexpr int kGroupM = CG == 1 ? DLLM_GROUP_M1 : DLLM_GROUP_M2;
+  // Instruction descriptors.  kind::f16: fp32 accumulator (bits 4-5 = 1), A and B bf16 (bits
+  // 7-9, 10-12 = 1).  kind::mxf4: A and B E2M1 (bits 7-9, 10-11 = 1), E8M0 scales (bit 23), the
+  // scale bytes used of each TMEM word (bits 4-5 for B, 29-30 for A: 0 or 2).  Both K-major, N >> 3
+  // at bits 17-22, M >> 4 at bits 24-28.
+  static constexpr uint32_t kIdesc =
+      (Op::kMx4 ? (1u << 7) | (1u << 10) | (1u << 23) : (1u << 4) | (1u << 7) | (1u << 10)) |
+      (static_cast<uint32_t>(Op::BN >> 3) << 17) | (static_cast<uint32_t>(BM >> 4) << 24);
+};
+
+template <class Op>
+constexpr int smem_bytes() {
+  return Cfg<1, Op>::SMEM_BYTES > Cfg<2, Op>::SMEM_BYTES ? Cfg<1, Op>::SMEM_BYTES : Cfg<2, Op>::SMEM_BYTES;
+}
+
+// lm::Plan counts vocabulary tiles of lm::BN columns; a V that has as many of those as the real
+// one has tiles of Op::BN.
+template <class Op>
+__host__ __device__ inline int plan_v(int V) {
+  return (V + Op::BN - 1) / Op::BN * lm::BN;
+}
+
+// ---- MXFP4 tensor-core wrappers ---------------------------------------------------------
+// D (+)= (A * scales) * (B * scales)^T, block scaled, 32 elements per scale.
+template <int CG>
+__device__ __forceinline__ void umma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+  if constexpr (CG == 1)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+
+// One scale tile (512 bytes: 32 rows of 16) from shared memory to 4 TMEM columns, in each lane
+// quadrant; with CG = 2 in both CTAs of the pair, each from its own shared memory.
+template <int CG>
+__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint64_t desc) {
+  if constexpr (CG == 1)
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+  else
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+// Shared-memory descriptor of a scale tile: no swizzle, 8 rows of 16 bytes contiguous, 128
+// bytes from one such group to the next.
+__device__ __forceinline__ uint64_t scale_desc(uint32_t smem_addr) {
+  return static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(128u >> 4) << 32) |
+         (static_cast<uint64_t>(1u) << 46);
+}
+
+template <int CG, class Op>
+struct Smem {
+  uint8_t *a, *b, *sfa, *sfb;                        // kStages tiles each
+  uint64_t *full, *empty, *tfull, *tempty, *drain, *epi_bar;
+  uint32_t* tmem_slot;
+  int* abort_flag;
+  volatile int* last_flag;
+  struct RowStateRaw { float m, s, t, m2; int a; };
+  RowStateRaw* comb;
+
+  __device__ __forceinline__ explicit Smem(uint8_t* raw) {
+    using C = Cfg<CG, Op>;
+    a = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    b = a + C::kStages * C::A_BYTES;
+    sfa = b + C::kStages * C::B_BYTES;
+    sfb = sfa + C::kStages * Op::SFA;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sfb + C::kStages * Op::SFB);
+    full = bars;
+    empty = bars + C::kStages;
+    tfull = bars + 2 * C::kStages;
+    tempty = tfull + 2;
+    drain = tfull + 4;
+    epi_bar = tfull + 5;
+    tmem_slot = reinterpret_cast<uint32_t*>(tfull + 6);
+    abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
+    last_flag = abort_flag + 1;
+    comb = reinterpret_cast<RowStateRaw*>(reinterpret_cast<uint8_t*>(bars) + 256);
+  }
+};
+
+struct Maps {
+  const CUtensorMap* a;      // Hm (or its codes): box of 32 rows (CG = 1) or 128 (CG = 2)
+  const CUtensorMap* b;      // W (or its codes): box of Op::BN / CG rows
+  const CUtensorMap* sa;     // scales of Hm: box of one tile row, 1024 bytes
+  const CUtensorMap* sb;     // scales of W: box of two tile rows, 1024 bytes
+};
+
+struct Problem {
+  int n_cap, V, d, L;
+  const int* row_idx;
+  Partials part;
+  long long part_cap;
+  int* unit_ctr;
+  Outputs out;
+  int* status;
+};
+
+template <int CG, class Op, bool kRules, bool kExt>
+__device__ __forceinline__ void run(uint8_t* smem_raw, const Maps& tm, int count_raw, const Problem& p,
+                                    const dllm_logit_rules& rule_set) {
+  using C = Cfg<CG, Op>;
+  constexpr int BN = Op::BN;
+  Smem<CG, Op> sm(smem_raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = CG == 1 ? 0u : cluster_ctarank();
+  const bool leader = rank == 0;
+  int* const status = p.status;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(smem_u32(&sm.full[s]), 1);
+      mbar_init(smem_u32(&sm.empty[s]), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(smem_u32(&sm.tfull[b]), 1);
+      mbar_init(smem_u32(&sm.tempty[b]), CG * kEpiWarps);
+    }
+    mbar_init(smem_u32(sm.drain), 1);
+    mbar_init(smem_u32(sm.epi_bar), kEpiWarps);
+    *sm.abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(tm.a);
+    tma_prefetch_desc(tm.b);
+    if constexpr (Op::kMx4) {
+      tma_prefetch_desc(tm.sa);
+      tma_prefetch_desc(tm.sb);
+    }
+  }
+  if (warp == 1) {
+    if constexpr (CG == 1) {
+      tmem_alloc(smem_u32(sm.tmem_slot), 512);
+      tmem_relinquish();
+    } else {
+      tmem_alloc_pair(smem_u32(sm.tmem_slot), 512);
+      tmem_relinquish_pair();
+    }
+  }
+  tc_fence_before();
+  if constexpr (CG == 1) __syncthreads();
+  else cluster_sync();          // barriers of both CTAs initialised before any remote use
+  tc_fence_after();
+  const uint32_t tmem_base = *sm.tmem_slot;
+  volatile int* abort_flag = sm.abort_flag;
+
+  const int count = count_raw < 0 ? 0 : (count_raw > p.n_cap ? p.n_cap : count_raw);
+  const Plan pl = Plan::make(count, plan_v<Op>(p.V), static_cast<int>(gridDim.x) / CG, C::kGroupM, C::BM);
+  const int holder = static_cast<int>(blockIdx.x) / CG;
+  const int KB = (p.d + Op::BK - 1) / Op::BK;
+  uint32_t armed_mask = 0, armed_parity = 0;      // as in lm::lmhead_run
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ------------------------------ TMA producer ------------------------------
+      uint32_t it = 0;
+      constexpr int kPace = CG == 2 ? DLLM_PAIR_PACE : 0;      // see lm::lmhead_run
+      constexpr int kMates = 40;
+      int* const progress = p.unit_ctr + ((p.n_cap + 127) / 128 + 2);
+      int started = 0;
+      int seen[kMates];
+#pragma unroll
+      for (int j = 0; j < kMates; ++j) seen[j] = 0;
+      auto pace = [&](int m_tile) -> bool {
+        if (kPace <= 0 || pl.ngroups < 2 || pl.rem || pl.gmax > kMates) return true;
+        const int g = m_tile / pl.gmax;
+        if (pl.group_size(g) != pl.gmax) return true;
+        if (rank == 0) st_relaxed_gpu(progress + holder, started);
+        const int first = (holder / pl.gmax) * pl.gmax;
+        const int need = started - kPace;
+        bool behind = false;
+#pragma unroll
+        for (int j = 0; j < kMates; ++j) behind |= j < pl.gmax && seen[j] < need;
+        if (behind) {
+          const unsigned long long t0 = globaltimer_ns();
+          for (;;) {
+            bool lag = false;
+            for (int j = 0; j < pl.gmax; ++j) lag |= ld_relaxed_gpu(progress + first + j) < need;
+            if (!lag) break;
+            if (*abort_flag) return false;
+            if (globaltimer_ns() - t0 > kWaitLimitNs) {
+              atomicOr(status, kStatusTimeout);
+              *abort_flag = 1;
+              return false;
+            }
+            __nanosleep(128);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < kMates; ++j)
+          if (j < pl.gmax) seen[j] = ld_relaxed_gpu(progress + first + j);
+        return true;
+      };
+      auto load_tile = [&](int m_tile, int n) -> bool {
+        if (!pace(m_tile)) return false;
+        ++started;
+        const int a_row = m_tile * C::BM + static_cast<int>(rank) * C::BM_CTA;
+        const int b_row = n * BN + static_cast<int>(rank) * C::B_ROWS;
+        const int valid = count - a_row;
+        const int boxes = valid >= C::BM_CTA ? 4 : (valid + 31) / 32;          // CG = 1: valid >= 1
+        for (int kb = 0; kb < KB; ++kb, ++it) {
+          const int s = it % C::kStages;
+          const uint32_t ph = (it / C::kStages) & 1u;
+          if (!mbar_wait(smem_u32(&sm.empty[s]), ph ^ 1u, abort_flag, status)) return false;
+#ifdef DLLM_FAULT_SKIP_STAGE
+          if (it == DLLM_FAULT_SKIP_STAGE) continue;
+#endif
+          const uint32_t fb = smem_u32(&sm.full[s]);
+          armed_mask |= 1u << s;
+          armed_parity = (armed_parity & ~(1u << s)) | (ph << s);
+          // x: elements of the map's type (bf16, bytes of codes, 8-byte words of scales)
+          const int x = kb * (Op::kMx4 ? 128 : 64);
+          const uint32_t da = smem_u32(sm.a + s * C::A_BYTES), db = smem_u32(sm.b + s * C::B_BYTES);
+          if constexpr (CG == 1) {
+            mbar_arrive_expect_tx(fb, C::STAGE_BYTES - (4 - boxes) * (C::A_BYTES / 4));
+            for (int i = 0; i < boxes; ++i)
+              tma_load_2d(da + i * (C::A_BYTES / 4), tm.a, fb, x, a_row + 32 * i);
+            tma_load_2d(db, tm.b, fb, x, b_row);
+            if constexpr (Op::kMx4) {
+              tma_load_2d(smem_u32(sm.sfa + s * Op::SFA), tm.sa, fb, x, a_row / 128);
+              tma_load_2d(smem_u32(sm.sfb + s * Op::SFB), tm.sb, fb, x, n * BN / 128);
+            }
+          } else {
+            if (leader) mbar_arrive_expect_tx(fb, CG * C::STAGE_BYTES);
+            const uint32_t fl = fb & kPeerBitMask;
+            tma_load_2d_pair(da, tm.a, fl, x, a_row);
+            tma_load_2d_pair(db, tm.b, fl, x, b_row);
+            if constexpr (Op::kMx4) {
+              tma_load_2d_pair(smem_u32(sm.sfa + s * Op::SFA), tm.sa, fl, x, a_row / 128);
+              tma_load_2d_pair(smem_u32(sm.sfb + s * Op::SFB), tm.sb, fl, x, n * BN / 128);
+            }
+          }
+        }
+        return true;
+      };
+      lm::for_each_tile(pl, holder, load_tile);
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && leader) {
+      // ------------------------------ MMA issuer --------------------------------
+      uint32_t it = 0, tile = 0;
+      auto mma_tile = [&](int, int n) -> bool {
+        const uint32_t buf = tile & 1u, tph = (tile >> 1) & 1u;
+        if (!mbar_wait(smem_u32(&sm.tempty[buf]), tph ^ 1u, abort_flag, status)) return false;
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + buf * BN;
+        for (int kb = 0; kb < KB; ++kb, ++it) {
+          const int s = it % C::kStages;
+          const uint32_t ph = (it / C::kStages) & 1u;
+          if (!mbar_wait(smem_u32(&sm.full[s]), ph, abort_flag, status)) return false;
+          tc_fence_after();
+          const uint64_t adesc = sw128_kmajor_desc(smem_u32(sm.a + s * C::A_BYTES));
+          const uint64_t bdesc = sw128_kmajor_desc(smem_u32(sm.b + s * C::B_BYTES));
+          if constexpr (!Op::kMx4) {
+#pragma unroll
+            for (int k = 0; k < Op::BK / Op::UK; ++k)
+              lm::mma_issue<CG>(d_tmem, adesc + 2 * k, bdesc + 2 * k, C::kIdesc, (kb | k) != 0 ? 1u : 0u);
+          } else {
+            // d is a multiple of 64, so the last stage holds 1 to 4 steps of K = 64; a scale
+            // tile covers two of them (bytes 0, 1 and 2, 3 of its words)
+            const int left = (p.d - kb * Op::BK) / Op::UK;
+            const int steps = left < 4 ? left : 4;
+            const uint32_t sf = tmem_base + 2 * BN + s * Op::kSfCols;
+            const uint64_t sa = scale_desc(smem_u32(sm.sfa + s * Op::SFA));
+            const uint64_t sb = scale_desc(smem_u32(sm.sfb + s * Op::SFB));
+#pragma unroll
+            for (int g = 0; g < 2; ++g)
+              if (2 * g < steps) {
+                tmem_cp_scales<CG>(sf + 4 * g, sa + 32 * g);              // 512 bytes apart
+                tmem_cp_scales<CG>(sf + 8 + 8 * g, sb + 32 * g);
+                tmem_cp_scales<CG>(sf + 8 + 8 * g + 4, sb + 64 + 32 * g);
+              }
+            const uint32_t sfb = sf + 8 + ((n * BN) % 128 != 0 ? 2 : 0);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (k < steps)
+                umma_mxf4<CG>(d_tmem, adesc + 2 * k, bdesc + 2 * k,
+                              C::kIdesc | ((k & 1) ? (2u << 4) | (2u << 29) : 0u), sf + 4 * (k >> 1),
+                              sfb + 8 * (k >> 1), (kb | k) != 0 ? 1u : 0u);
+          }
+          lm::mma_commit_all<CG>(smem_u32(&sm.empty[s]));
+        }
+        lm::mma_commit_all<CG>(smem_u32(&sm.tfull[buf]));
+        ++tile;
+        return true;
+      };
+      if (!lm::for_each_tile(pl, holder, mma_tile)) {
+        lm::mma_commit_all<CG>(smem_u32(sm.drain));       // no MMA may outlive TMEM
+        mbar_wait_drain(smem_u32(sm.drain), 0u, status);
+      }
+    }
   } else {
-    const uint8_t c = (a ? o.Hq : o.Wq)[r * (d / 2) + k / 2];
-    const uint8_t s = (a ? o.Hs : o.Ws)[4 * mx4::scale_word(r, k >> 7, (d + 127) / 128) + ((k >> 5) & 3)];
-    return mx4::e2m1_value(k & 1 ? c >> 4 : c & 15) * mx4::e8m0_value(s);
+    // -------------------------------- epilogue ---------------------------------
+    const int q = warp & 3;                      // TMEM lane quadrant of this warp
+    const int half = (warp - 2) >> 2;            // which half of a tile's columns
+    constexpr int kChunks = BN / 64;             // 32-column chunks of a half
+    const int row_in_cta = q * 32 + lane;
+    const int row_in_tile = static_cast<int>(rank) * C::BM_CTA + row_in_cta;
+    const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + half * (BN / 2);
+    uint32_t tile = 0, epi_phase = 0, units_done = 0;
+    bool ok = true, live = false;                // live: this warp holds a masked row of the m-tile
+    rules::RowRules rr = rules::no_rules();
+    auto enter_m_tile = [&](int m_tile) {
+      live = m_tile * C::BM + row_in_tile - lane < count;
+      if constexpr (kRules) {
+        const int row = m_tile * C::BM + row_in_tile;
+        rr = row < count ? rules::row_rules(rule_set, p.row_idx[row], p.L, status) : rules::no_rules();
+        __syncwarp();
+      }
+    };
+    // all epilogue warps meet; false (warp-uniform) if the CTA is aborting
+    auto epi_sync = [&]() -> bool {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(sm.epi_bar));
+      const bool got = mbar_wait(smem_u32(sm.epi_bar), epi_phase, abort_flag, status);
+      epi_phase ^= 1u;
+      return __all_sync(0xffffffffu, got);
+    };
+    // fold this warp's half of the next accumulator (vocabulary tile n) into st
+    auto consume = [&](int n, rules::State& st) -> bool {
+      const uint32_t buf = tile & 1u, tph = (tile >> 1) & 1u;
+      const int first = n * BN + half * (BN / 2);
+      if constexpr (kRules) {
+        if (live) {
+          rules::Words w[kChunks];
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c) w[c] = rules::load_words(first + 32 * c, p.V, rr);
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c) rules::prefetch_chunk(first + 32 * c, p.V, rr, w[c]);
+        }
+      }
+      const bool got = mbar_wait(smem_u32(&sm.tfull[buf]), tph, abort_flag, status);
+      if (!__all_sync(0xffffffffu, got)) return false;
+      tc_fence_after();
+      if (live) {
+        const uint32_t taddr = lane_base + buf * BN;
+#pragma unroll 1
+        for (int c = 0; c < kChunks; ++c) {
+          float v[32];
+          const int col0 = first + c * 32;
+          rules::Words w;
+          if constexpr (kRules) w = rules::load_words(col0, p.V, rr);
+          tmem_ld32(taddr + c * 32, v);
+          tmem_ld_wait();
+          if constexpr (kRules) {
+            if (!rules::shape_chunk(v, col0, p.V, rr, w)) continue;
+          } else if (col0 + 32 > p.V) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (col0 + j >= p.V) v[j] = -INFINITY;
+          }
+          rules::fold<kExt>(v, col0, st);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      // release the accumulator: the leader's MMA waits for the epilogues of both CTAs
+      if (lane == 0) {
+        if constexpr (CG == 1) mbar_arrive(smem_u32(&sm.tempty[buf]));
+        else mbar_arrive_cluster(smem_u32(&sm.tempty[buf]), 0u);
+      }
+      ++tile;
+      return true;
+    };
+    auto write_result = [&](int row, const RowState& st) {
+      int t;
+      float c, l, e, mg;
+      rules::finish(st, t, c, l, e, mg);
+      p.out.tok[row] = t;
+      p.out.conf[row] = c;
+      p.out.lse[row] = l;
+      if constexpr (kExt) {
+        if (p.out.entropy) p.out.entropy[row] = e;
+        if (p.out.margin) p.out.margin[row] = mg;
+      }
+    };
+    auto put = [&](int block, int r, const RowState& st) {
+      auto& c = sm.comb[block * C::BM_CTA + r];
+      c.m = st.m;
+      c.s = st.s;
+      c.t = st.t;
+      c.m2 = st.m2;
+      c.a = st.a;
+    };
+    auto add = [&](int block, int r, RowState& st) {
+      const auto& c = sm.comb[block * C::BM_CTA + r];
+      rules::merge<kExt>(st, c.m, c.s, c.a, c.t, c.m2);
+    };
+    auto add_partial = [&](long long e, RowState& st) {
+      rules::merge<kExt>(st, __ldcg(p.part.m + e), __ldcg(p.part.s + e), __ldcg(p.part.a + e),
+                         kExt ? __ldcg(p.part.t + e) : 0.f, kExt ? __ldcg(p.part.m2 + e) : 0.f);
+    };
+    // A finished (m-tile, slot): the two halves' states are joined; the result itself when the
+    // m-tile has a single unit, else a partial; the last of the m-tile's units to finish merges
+    // its rows.
+    auto finish = [&](int g, const Unit& u, int m_local, int slot, const rules::State& part_st) -> bool {
+      const int m_tile = g * pl.gmax + m_local;
+      const int row = m_tile * C::BM + row_in_tile;
+      const bool valid = row < count;
+      int j_lo = 0, j_hi = -1;
+      if (pl.rem) pl.leftovers_of(m_local, u.G, j_lo, j_hi);
+      const int units = u.P + (j_hi >= j_lo ? j_hi - j_lo + 1 : 0);
+      RowState st = part_st.value();
+      // two blocks in turn: the next unit's states may be written while these are still read
+      const int block = units_done++ & 1;
+      if (half == 1) put(block, row_in_cta, st);
+      if (!epi_sync()) return false;
+      if (half == 0) add(block, row_in_cta, st);
+      if (units == 1) {
+        if (half == 0 && valid) write_result(row, st);
+        return true;
+      }
+      if (half == 0 && valid) {
+        const long long e = pl.part_index(g, u.G, slot, m_local * C::BM + row_in_tile);
+        if (e < p.part_cap) {
+          p.part.m[e] = st.m;
+          p.part.s[e] = st.s;
+          p.part.a[e] = st.a;
+          if constexpr (kExt) {
+            p.part.t[e] = st.t;
+            p.part.m2[e] = st.m2;
+          }
+        } else {
+          atomicOr(status, kStatusBounds);             // cannot happen: workspace sized for it
+        }
+      }
+      // Writers fence before the counter increment; the last arriver fences after it and reads
+      // the partials through L2.
+      __threadfence();
+      if (!epi_sync()) return false;
+      if (threadIdx.x == 2 * 32) {
+        const int old = atomicAdd(&p.unit_ctr[m_tile * CG + static_cast<int>(rank)], 1);
+        *sm.last_flag = old == units - 1 ? 1 : 0;
+      }
+      if (!epi_sync()) return false;
+      if (!*sm.last_flag) return true;
+      __threadfence();
+      const int row0 = m_tile * C::BM + static_cast<int>(rank) * C::BM_CTA;   // CTA's first row
+      const int n_valid = count - row0 < C::BM_CTA ? count - row0 : C::BM_CTA;
+      const long long base0 = pl.part_index(g, u.G, 0, m_local * C::BM + static_cast<int>(rank) * C::BM_CTA);
+      const long long stride = static_cast<long long>(u.G) * C::BM;
+      auto slot_of = [&](int i) { return i < u.P ? i : u.P + j_lo + (i - u.P); };
+      if (n_valid <= 32) {
+        for (int r = warp - 2; r < n_valid; r += kEpiWarps) {
+          RowState acc;
+          acc.reset();
+          for (int i = lane; i < units; i += 32) add_partial(base0 + slot_of(i) * stride + r, acc);
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) {
+            const float m = __shfl_xor_sync(0xffffffffu, acc.m, o), s = __shfl_xor_sync(0xffffffffu, acc.s, o);
+            const int a = __shfl_xor_sync(0xffffffffu, acc.a, o);
+            const float t = kExt ? __shfl_xor_sync(0xffffffffu, acc.t, o) : 0.f;
+            const float m2 = kExt ? __shfl_xor_sync(0xffffffffu, acc.m2, o) : 0.f;
+            rules::merge<kExt>(acc, m, s, a, t, m2);
+          }
+          if (lane == 0) write_result(row0 + r, acc);
+        }
+      } else {
+        // warp quarter q takes the slots [q * units / 4, (q + 1) * units / 4), of the CTA's rows
+        // 64 * half + lane and + 32 more; the quarters meet in shared memory
+        const int s0 = q * units / 4, s1 = (q + 1) * units / 4;
+        RowState acc[2];
+        acc[0].reset();
+        acc[1].reset();
+#pragma unroll 4
+        for (int i = s0; i < s1; ++i) {
+          const long long e = base0 + slot_of(i) * stride + 64 * half + lane;
+          if (64 * half + lane < n_valid) add_partial(e, acc[0]);
+          if (64 * half + lane + 32 < n_valid) add_partial(e + 32, acc[1]);
+        }
+        put(q, 64 * half + lane, acc[0]);
+        put(q, 64 * half + lane + 32, acc[1]);
+        if (!epi_sync()) return false;
+        if (half == 0 && valid) {
+          RowState fin;
+          fin.reset();
+#pragma unroll
+          for (int k = 0; k < 4; ++k) add(k, row_in_cta, fin);
+          write_result(row, fin);
+        }
+        if (!epi_sync()) return false;           // the blocks are free for the next unit
+      }
+      return true;
+    };
+
+    for (int g = 0; g < pl.ngroups && ok; ++g) {
+      Unit u;
+      if (!lm::unit_of(pl, g, holder, u)) continue;
+      rules::State st;
+      st.reset();
+      if (u.leftover) {
+        int cur = -1;
+        for (long long i = u.i0; i < u.i1 && ok; ++i) {
+          const int m_local = static_cast<int>(i / pl.rr);
+          const int n = u.P * pl.rb + static_cast<int>(i % pl.rr);
+          if (m_local != cur) {
+            if (cur >= 0) ok = finish(g, u, cur, u.p, st);
+            cur = m_local;
+            st.reset();
+            enter_m_tile(g * pl.gmax + m_local);
+          }
+          if (ok && !consume(n, st)) ok = false;
+        }
+        if (ok && cur >= 0) ok = finish(g, u, cur, u.p, st);
+      } else {
+        enter_m_tile(u.m_tile);
+        for (int n = u.n0; n < u.n1 && ok; ++n)
+          if (!consume(n, st)) ok = false;
+        if (ok) ok = finish(g, u, u.m_local, u.p, st);
+      }
+    }
+  }
+
+  tc_fence_before();
+  if constexpr (CG == 1) __syncthreads();
+  else cluster_sync();          // neither CTA leaves while its peer may still touch its smem
+  bool aborted = *abort_flag != 0;
+  if constexpr (CG == 2) {
+    aborted = aborted || ld_shared_cluster_s32(smem_u32(sm.abort_flag), rank ^ 1u) != 0;
+    cluster_sync();             // the peer's shared memory stays alive until both have read
+  }
+  if (aborted) {                // loads already issued land before shared memory is released
+    if (warp == 0 && lane == 0 && (CG == 1 || leader)) {
+      const unsigned long long deadline = globaltimer_ns() + kWaitLimitNs;
+      for (int s = 0; s < C::kStages; ++s)
+        if (armed_mask & (1u << s))
+          if (!mbar_wait_until(smem_u32(&sm.full[s]), (armed_parity >> s) & 1u, deadline, status)) break;
+    }
+    if constexpr (CG == 1) __syncthreads();
+    else cluster_sync();
+  }
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    if constexpr (CG == 1) tmem_dealloc(tmem_base, 512);
+    else tmem_dealloc_pair(tmem_base, 512);
   }
 }
 
-template <bool kMx4, bool kExt>
-__global__ void __launch_bounds__(kThreads)
-shaped_kernel(const Operands o, const int* __restrict__ count_ptr, int n_cap, int V, int d, int L,
-              const dllm_logit_rules r, const int* __restrict__ row_idx, const lm::Partials part,
-              int n_split, int* __restrict__ status) {
-  __shared__ float a[BK][BM + 1], b[BK][BN + 1];
-  __shared__ float z[BM][BN + 1];
+// Launched in clusters of two CTAs; variant 0 chooses the body from the masked count as
+// lm::lmhead_auto_kernel does, 1 and 2 force it (test hook).
+template <class Op, bool kRules, bool kExt>
+__global__ void __launch_bounds__(kThreads, 1)
+shaped_kernel(const __grid_constant__ CUtensorMap tmA1, const __grid_constant__ CUtensorMap tmA2,
+              const __grid_constant__ CUtensorMap tmB1, const __grid_constant__ CUtensorMap tmB2,
+              const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
+              const int* __restrict__ count_ptr, int variant, const Problem p,
+              const __grid_constant__ dllm_logit_rules rule_set) {
+  extern __shared__ uint8_t smem_raw[];
   pdl_wait();
   pdl_launch_dependents();
-  int n = *count_ptr;
-  n = n < 0 ? 0 : (n > n_cap ? n_cap : n);
-  const int r0 = blockIdx.x * BM;
-  if (r0 >= n) return;
-  const int tiles = (V + BN - 1) / BN;
-  const int t0 = static_cast<int>(static_cast<long long>(blockIdx.y) * tiles / n_split);
-  const int t1 = static_cast<int>(static_cast<long long>(blockIdx.y + 1) * tiles / n_split);
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int row = r0 + threadIdx.x;                        // threads 0..63: one row each
-  rules::RowRules rr = rules::no_rules();
-  if (threadIdx.x < BM && row < n) rr = rules::row_rules(r, row_idx[row], L, status);
-  lm::RowState st;
-  st.reset();
-  for (int t = t0; t < t1; ++t) {
-    float acc[4][4] = {};
-    for (int k0 = 0; k0 < d; k0 += BK) {
-      for (int i = threadIdx.x; i < BM * BK; i += kThreads) {
-        const int rr_ = i / BK, k = i % BK;
-        a[k][rr_] = r0 + rr_ < n ? element<kMx4>(o, true, r0 + rr_, k0 + k, d) : 0.f;
-        b[k][rr_] = t * BN + rr_ < V ? element<kMx4>(o, false, t * BN + rr_, k0 + k, d) : 0.f;
-      }
-      __syncthreads();
-      for (int k = 0; k < BK; ++k)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a[k][ty * 4 + i], b[k][tx * 4 + j], acc[i][j]);
-      __syncthreads();
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) z[ty * 4 + i][tx * 4 + j] = acc[i][j];
-    __syncthreads();
-    if (threadIdx.x < BM) {
-      for (int c = 0; c < BN; c += 32) {
-        float v[32];
-#pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = z[threadIdx.x][c + j];
-        rules::shape_chunk(v, t * BN + c, V, rr);
-        rules::fold<kExt>(v, t * BN + c, st);
-      }
-    }
-    __syncthreads();
-  }
-  if (threadIdx.x < BM && row < n) {
-    const long long e = static_cast<long long>(blockIdx.y) * n_cap + row;
-    part.m[e] = st.m;
-    part.s[e] = st.s;
-    part.a[e] = st.a;
-    if constexpr (kExt) {
-      part.t[e] = st.t;
-      part.m2[e] = st.m2;
-    }
-  }
-}
-
-template <bool kExt>
-__global__ void __launch_bounds__(kThreads)
-shaped_merge_kernel(const lm::Partials part, const int* __restrict__ count_ptr, int n_cap, int n_split,
-                    const lm::Outputs out) {
-  pdl_wait();
-  pdl_launch_dependents();
-  int n = *count_ptr;
-  n = n < 0 ? 0 : (n > n_cap ? n_cap : n);
-  for (int row = blockIdx.x * kThreads + threadIdx.x; row < n; row += gridDim.x * kThreads) {
-    lm::RowState st;
-    st.reset();
-    for (int j = 0; j < n_split; ++j) {
-      const long long e = static_cast<long long>(j) * n_cap + row;
-      rules::merge<kExt>(st, part.m[e], part.s[e], part.a[e], kExt ? part.t[e] : 0.f,
-                         kExt ? part.m2[e] : 0.f);
-    }
-    int t;
-    float c, l, en, mg;
-    rules::finish(st, t, c, l, en, mg);
-    out.tok[row] = t;
-    out.conf[row] = c;
-    out.lse[row] = l;
-    if constexpr (kExt) {
-      if (out.entropy) out.entropy[row] = en;
-      if (out.margin) out.margin[row] = mg;
-    }
-  }
+  const int c = *count_ptr;
+  if ((variant == 0 ? lm::auto_variant(c) : variant) == 2)
+    run<2, Op, kRules, kExt>(smem_raw, Maps{&tmA2, &tmB2, &tmSA, &tmSB}, c, p, rule_set);
+  else
+    run<1, Op, kRules, kExt>(smem_raw, Maps{&tmA1, &tmB1, &tmSA, &tmSB}, c, p, rule_set);
 }
 
 }  // namespace shaped

@@ -140,12 +140,12 @@ dllm_status device_state(DeviceState** out) {
            cudaFuncSetAttribute(lm::lmhead_auto_kernel<lm::kModeStats>, smem_attr, lm::kAutoSmemBytes) ||
            cudaFuncSetAttribute(lm::lmhead_auto_kernel<lm::kModeStatsExt>, smem_attr, lm::kAutoSmemBytes) ||
            cudaFuncSetAttribute(lm::lmhead_auto_kernel<lm::kModeDebugStore>, smem_attr, lm::kAutoSmemBytes) ||
-           cudaFuncSetAttribute(shaped::shaped_kernel<shaped::Bf16, true, false>, smem_attr, shaped::smem_bytes<shaped::Bf16>()) ||
-           cudaFuncSetAttribute(shaped::shaped_kernel<shaped::Bf16, true, true>, smem_attr, shaped::smem_bytes<shaped::Bf16>()) ||
-           cudaFuncSetAttribute(shaped::shaped_kernel<shaped::Mx4, true, false>, smem_attr, shaped::smem_bytes<shaped::Mx4>()) ||
-           cudaFuncSetAttribute(shaped::shaped_kernel<shaped::Mx4, true, true>, smem_attr, shaped::smem_bytes<shaped::Mx4>()) ||
-           cudaFuncSetAttribute(shaped::shaped_kernel<shaped::Mx4, false, false>, smem_attr, shaped::smem_bytes<shaped::Mx4>()) ||
-           cudaFuncSetAttribute(shaped::shaped_kernel<shaped::Mx4, false, true>, smem_attr, shaped::smem_bytes<shaped::Mx4>()) ||
+           cudaFuncSetAttribute(shaped::shaped_kernel<shaped::Bf16, true, false>, smem_attr, shaped::kSmemBytes) ||
+           cudaFuncSetAttribute(shaped::shaped_kernel<shaped::Bf16, true, true>, smem_attr, shaped::kSmemBytes) ||
+           cudaFuncSetAttribute(shaped::shaped_kernel<shaped::Mx4, true, false>, smem_attr, shaped::kSmemBytes) ||
+           cudaFuncSetAttribute(shaped::shaped_kernel<shaped::Mx4, true, true>, smem_attr, shaped::kSmemBytes) ||
+           cudaFuncSetAttribute(shaped::shaped_kernel<shaped::Mx4, false, false>, smem_attr, shaped::kSmemBytes) ||
+           cudaFuncSetAttribute(shaped::shaped_kernel<shaped::Mx4, false, true>, smem_attr, shaped::kSmemBytes) ||
            cudaFuncSetAttribute(rules::token_count_kernel, smem_attr, rules::kCountMaxSlice * 4)))
         st.err = DLLM_ERR_CUDA;
       if (st.err == DLLM_OK) {
@@ -562,7 +562,7 @@ dllm_status make_map(CUtensorMap* tm, CUtensorMapDataType type, int bytes, const
 // The GEMM on prepared rows: one launch in clusters of two CTAs.
 template <class Op>
 dllm_status launch_shaped(const ShapedArgs& x, const DeviceState& ds, const WsLayout& w,
-                          const lm::Partials& part, const lm::Outputs& outs) {
+                          const lm::Outputs& outs) {
   const LogitsArgs& a = x.a;
   if (ds.pairs < 1) return DLLM_ERR_DEVICE;
   uint8_t* ws = static_cast<uint8_t*>(a.ws);
@@ -597,7 +597,7 @@ dllm_status launch_shaped(const ShapedArgs& x, const DeviceState& ds, const WsLa
   cudaLaunchAttribute attr[2];
   cfg.gridDim = dim3(2 * ds.pairs, 1, 1);
   cfg.blockDim = dim3(shaped::kThreads, 1, 1);
-  cfg.dynamicSmemBytes = shaped::smem_bytes<Op>();
+  cfg.dynamicSmemBytes = shaped::kSmemBytes;
   cfg.stream = a.s;
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -607,7 +607,11 @@ dllm_status launch_shaped(const ShapedArgs& x, const DeviceState& ds, const WsLa
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  const shaped::Problem p{static_cast<int>(w.rows), a.V, a.d, a.L, a.row_idx, part, w.part_cap,
+  // partials: 16 bytes each in the first four of the workspace's partial arrays (which are one
+  // piece), the argmax in the fifth
+  const shaped::Problem p{static_cast<int>(w.rows), a.V, a.d, a.L, a.row_idx,
+                          reinterpret_cast<float4*>(ws + w.pm_off), reinterpret_cast<int*>(ws + w.pm2_off),
+                          w.part_cap,
                           reinterpret_cast<int*>(ws + w.ctr_off), outs, ds.status};
   const dllm_logit_rules rules = x.rules ? *x.rules : dllm_logit_rules{};
   const int* count = a.count;
@@ -671,11 +675,8 @@ dllm_status run_shaped(const ShapedArgs& x) {
       return DLLM_ERR_CUDA;
     count_launch();
   }
-  const lm::Partials part{reinterpret_cast<float*>(ws + w.pm_off), reinterpret_cast<float*>(ws + w.ps_off),
-                          reinterpret_cast<int*>(ws + w.pa_off), reinterpret_cast<float*>(ws + w.pt_off),
-                          reinterpret_cast<float*>(ws + w.pm2_off)};
   const lm::Outputs outs{a.tok, a.conf, a.lse, a.entropy, a.margin, a.raw, 0};
-  return mx4 ? launch_shaped<shaped::Mx4>(x, *ds, w, part, outs) : launch_shaped<shaped::Bf16>(x, *ds, w, part, outs);
+  return mx4 ? launch_shaped<shaped::Mx4>(x, *ds, w, outs) : launch_shaped<shaped::Bf16>(x, *ds, w, outs);
 }
 
 dllm_status mx4_checks(const void* X, int dtype, bool f16_ok, int64_t rows, int32_t cols, int64_t ld,

@@ -9,12 +9,18 @@
 //             of K are 128 bytes, so a stage holds four times the K of a bf16 stage.  The
 //             scales of a stage are copied from shared memory to TMEM (tcgen05.cp, each 512-byte
 //             tile to 4 columns, replicated over the four lane quadrants) ahead of its MMAs.
-//             TMEM holds two accumulators and, per stage of the ring, the stage's scales; with
-//             192 columns a tile that is 2 x 192 + 5 x 24 = 504 of 512 columns.  A stage's
-//             scale columns are rewritten only after the MMAs that read them have released the
-//             stage.  A tile of 192 columns starts on a scale tile (128 rows of W) or in the
-//             middle of one: it takes two scale tiles and, if odd, starts two columns in.
-//   A rows    single CTAs load their rows of Hm in boxes of 32, only as many as are masked.
+//             TMEM holds two accumulators and the scales of five stages; with 192 columns a
+//             tile that is 2 x 192 + 5 x 24 = 504 of 512 columns.  Scale columns are rewritten
+//             only after the MMAs that read them have released their stage.  A tile of 192
+//             columns starts on a scale tile (128 rows of W) or in the middle of one: it takes
+//             two scale tiles and, if odd, starts two columns in.
+//   issue     four MMAs of a stage take 0.2 us, so the issuing warp runs converged, with
+//             warp-uniform operands, and elects a lane per instruction: from a lone lane the
+//             operands pass through vector registers and a stage took 0.53 us to issue.
+//   ring      as many stages as fit: what bounds the staging is the bytes in flight (a stage
+//             comes 2 us after it is asked for when every SM loads).
+//   A rows    single CTAs load their rows of Hm in boxes of 32, only as many as are masked,
+//             and give the rest of the tile's room to more stages.
 //   epilogue  eight warps: two per TMEM lane quadrant, each with half of a tile's columns (the
 //             rules and scores cost more instructions than the plain statistics, and four MXFP4
 //             tiles take the time of one bf16 tile).  rules::shape_chunk on each 32 logits, then
@@ -31,9 +37,7 @@ namespace dllm {
 namespace shaped {
 
 constexpr int kEpiWarps = 8;
-constexpr int kThreads = 64 + 32 * kEpiWarps;
 using lm::Outputs;
-using lm::Partials;
 using lm::Plan;
 using lm::RowState;
 using lm::Unit;
@@ -43,8 +47,7 @@ struct Bf16 {
   static constexpr int BN = 256;        // vocabulary entries per tile
   static constexpr int BK = 64;         // K per stage: 128 bytes
   static constexpr int UK = 16;         // K per tcgen05.mma
-  static constexpr int SFA = 0, SFB = 0, kSfCols = 0;
-  static constexpr int kStages1 = 4, kStages2 = 6;
+  static constexpr int SFA = 0, SFB = 0, kSfCols = 0, kSfRing = 0;
 };
 struct Mx4 {
   static constexpr bool kMx4 = true;
@@ -54,23 +57,32 @@ struct Mx4 {
   static constexpr int SFA = 1024;      // scale bytes per stage: 128 rows of Hm, 8 blocks
   static constexpr int SFB = 2048;      // 256 rows of W
   static constexpr int kSfCols = 24;    // TMEM columns of one stage's scales
-  static constexpr int kStages1 = 5, kStages2 = 5;
+  static constexpr int kSfRing = 5;     // stages whose scales TMEM holds
 };
+
+// Warps: TMA, MMA, two idle (an epilogue warp's number gives its TMEM lane quadrant), epilogue.
+constexpr int kEpiFirst = 4;
+constexpr int kThreads = 32 * (kEpiFirst + kEpiWarps);
+
+// Shared memory: barriers and flags, two blocks of row states (the halves of a tile meet there),
+// then the ring.
+constexpr int kMaxStages = 8;
+constexpr int kHeadBytes = 512;
+constexpr int kCombBytes = 2 * 128 * 20;
+constexpr int kRingOffset = 6144;
+constexpr int kSmemBytes = 232448;                   // all of a CTA's 227 KB
+constexpr int kRingBytes = kSmemBytes - 1024 - kRingOffset;
+static_assert(kHeadBytes + kCombBytes <= kRingOffset && kRingOffset % 1024 == 0, "shared-memory layout");
 
 template <int CG, class Op>
 struct Cfg {
   static constexpr int BM_CTA = 128;                 // rows per CTA (TMEM lanes)
   static constexpr int BM = BM_CTA * CG;             // rows per m-tile
   static constexpr int B_ROWS = Op::BN / CG;         // W rows staged per CTA per stage
-  static constexpr int A_BYTES = BM_CTA * 128;
+  static constexpr int A_BOX = 32 * 128;             // 32 rows of Hm
   static constexpr int B_BYTES = B_ROWS * 128;
-  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + Op::SFA + Op::SFB;
-  static constexpr int kStages = CG == 1 ? Op::kStages1 : Op::kStages2;
-  static constexpr int kCombBytes = 4 * BM_CTA * 20;
-  static constexpr int SMEM_BYTES = 1024 + kStages * STAGE_BYTES + 256 + kCombBytes;
-  static_assert(SMEM_BYTES <= 232448, "exceeds the 227 KB of shared memory of one CTA");
   static_assert(B_BYTES % 1024 == 0, "B tiles start on swizzle atoms");
-  static_assert(2 * Op::BN + kStages * Op::kSfCols <= 512, "exceeds TMEM");
+  static_assert(2 * Op::BN + Op::kSfRing * Op::kSfCols <= 512, "exceeds TMEM");
   static constexpr int kGroupM = CG == 1 ? DLLM_GROUP_M1 : DLLM_GROUP_M2;
   // Instruction descriptors.  kind::f16: fp32 accumulator (bits 4-5 = 1), A and B bf16 (bits
   // 7-9, 10-12 = 1).  kind::mxf4: A and B E2M1 (bits 7-9, 10-11 = 1), E8M0 scales (bit 23), the
@@ -80,11 +92,6 @@ struct Cfg {
       (Op::kMx4 ? (1u << 7) | (1u << 10) | (1u << 23) : (1u << 4) | (1u << 7) | (1u << 10)) |
       (static_cast<uint32_t>(Op::BN >> 3) << 17) | (static_cast<uint32_t>(BM >> 4) << 24);
 };
-
-template <class Op>
-constexpr int smem_bytes() {
-  return Cfg<1, Op>::SMEM_BYTES > Cfg<2, Op>::SMEM_BYTES ? Cfg<1, Op>::SMEM_BYTES : Cfg<2, Op>::SMEM_BYTES;
-}
 
 // lm::Plan counts vocabulary tiles of lm::BN columns; a V that has as many of those as the real
 // one has tiles of Op::BN.
@@ -131,33 +138,61 @@ __device__ __forceinline__ uint64_t scale_desc(uint32_t smem_addr) {
          (static_cast<uint64_t>(1u) << 46);
 }
 
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
+// Addresses in shared memory.  A stage: [Hm rows, boxes x 4 KB | W rows | scales of Hm | of W].
 template <int CG, class Op>
 struct Smem {
-  uint8_t *a, *b, *sfa, *sfb;                        // kStages tiles each
-  uint64_t *full, *empty, *tfull, *tempty, *drain, *epi_bar;
+  using C = Cfg<CG, Op>;
+  uint64_t *full, *empty;                            // per stage
+  uint64_t *tfull, *tempty, *drain, *epi_bar;
   uint32_t* tmem_slot;
   int* abort_flag;
   volatile int* last_flag;
   struct RowStateRaw { float m, s, t, m2; int a; };
   RowStateRaw* comb;
+  uint8_t* ring;
+  int stages;
+  uint32_t b_off, stage_bytes;
 
-  __device__ __forceinline__ explicit Smem(uint8_t* raw) {
-    using C = Cfg<CG, Op>;
-    a = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-    b = a + C::kStages * C::A_BYTES;
-    sfa = b + C::kStages * C::B_BYTES;
-    sfb = sfa + C::kStages * Op::SFA;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(sfb + C::kStages * Op::SFB);
-    full = bars;
-    empty = bars + C::kStages;
-    tfull = bars + 2 * C::kStages;
+  __device__ __forceinline__ Smem(uint8_t* raw, int boxes) {
+    uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    full = reinterpret_cast<uint64_t*>(base);
+    empty = full + kMaxStages;
+    tfull = empty + kMaxStages;
     tempty = tfull + 2;
     drain = tfull + 4;
     epi_bar = tfull + 5;
     tmem_slot = reinterpret_cast<uint32_t*>(tfull + 6);
     abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
     last_flag = abort_flag + 1;
-    comb = reinterpret_cast<RowStateRaw*>(reinterpret_cast<uint8_t*>(bars) + 256);
+    comb = reinterpret_cast<RowStateRaw*>(base + kHeadBytes);
+    ring = base + kRingOffset;
+    b_off = boxes * C::A_BOX;
+    stage_bytes = b_off + C::B_BYTES + Op::SFA + Op::SFB;
+    stages = kRingBytes / stage_bytes;
+    if (stages > kMaxStages) stages = kMaxStages;
+  }
+  __device__ __forceinline__ uint32_t a(int s) const { return smem_u32(ring) + s * stage_bytes; }
+  __device__ __forceinline__ uint32_t b(int s) const { return a(s) + b_off; }
+  __device__ __forceinline__ uint32_t sfa(int s) const { return b(s) + C::B_BYTES; }
+  __device__ __forceinline__ uint32_t sfb(int s) const { return sfa(s) + Op::SFA; }
+};
+
+// Position in the ring: stage, and the parity of its current use.
+struct Turn {
+  int s = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void next(int stages) {
+    if (++s == stages) {
+      s = 0;
+      ph ^= 1u;
+    }
   }
 };
 
@@ -171,26 +206,61 @@ struct Maps {
 struct Problem {
   int n_cap, V, d, L;
   const int* row_idx;
-  Partials part;
+  float4* part;              // per (split, row): m, s, t, m2
+  int* part_a;               // and the argmax
   long long part_cap;
   int* unit_ctr;
   Outputs out;
   int* status;
 };
 
+// The partials of one row in slots i0, i0 + step, .. below i1 (streams 0 .. P - 1, then remainder
+// holders from j_lo), merged.  All loads of a round are issued before any is used; kept out of
+// line so that its registers do not weigh on the epilogue's loop.
+template <bool kExt>
+__device__ __noinline__ RowState merge_slots(const float4* part, const int* part_a, long long base,
+                                             long long stride, int i0, int i1, int step, int P, int j_lo) {
+  constexpr int kRound = 8;
+  RowState acc;
+  acc.reset();
+#pragma unroll 1
+  for (; i0 < i1; i0 += kRound * step) {
+    float4 v[kRound];
+    int a[kRound];
+#pragma unroll
+    for (int k = 0; k < kRound; ++k) {
+      const int i = i0 + k * step;
+      const long long e = base + (i < P ? i : i + j_lo) * stride;
+      v[k] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+      a[k] = 0;
+      if (i < i1) {
+        v[k] = __ldcg(part + e);
+        a[k] = __ldcg(part_a + e);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kRound; ++k) rules::merge<kExt>(acc, v[k].x, v[k].y, a[k], v[k].z, v[k].w);
+  }
+  return acc;
+}
+
 template <int CG, class Op, bool kRules, bool kExt>
 __device__ __forceinline__ void run(uint8_t* smem_raw, const Maps& tm, int count_raw, const Problem& p,
                                     const dllm_logit_rules& rule_set) {
   using C = Cfg<CG, Op>;
   constexpr int BN = Op::BN;
-  Smem<CG, Op> sm(smem_raw);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  count_raw = __shfl_sync(0xffffffffu, count_raw, 0);              // warp-uniform, and known to be
+  const int count = count_raw < 0 ? 0 : (count_raw > p.n_cap ? p.n_cap : count_raw);
+  // boxes of 32 rows that hold a CTA's rows (one m-tile of fewer than 128 rows needs fewer)
+  const int a_boxes = CG == 2 || count >= C::BM_CTA ? 4 : (count > 0 ? (count + 31) / 32 : 1);
+  const Smem<CG, Op> sm(smem_raw, a_boxes);
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // uniform
   const uint32_t rank = CG == 1 ? 0u : cluster_ctarank();
   const bool leader = rank == 0;
   int* const status = p.status;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < C::kStages; ++s) {
+    for (int s = 0; s < sm.stages; ++s) {
       mbar_init(smem_u32(&sm.full[s]), 1);
       mbar_init(smem_u32(&sm.empty[s]), 1);
     }
@@ -224,10 +294,9 @@ __device__ __forceinline__ void run(uint8_t* smem_raw, const Maps& tm, int count
   if constexpr (CG == 1) __syncthreads();
   else cluster_sync();          // barriers of both CTAs initialised before any remote use
   tc_fence_after();
-  const uint32_t tmem_base = *sm.tmem_slot;
+  const uint32_t tmem_base = __shfl_sync(0xffffffffu, *sm.tmem_slot, 0);
   volatile int* abort_flag = sm.abort_flag;
 
-  const int count = count_raw < 0 ? 0 : (count_raw > p.n_cap ? p.n_cap : count_raw);
   const Plan pl = Plan::make(count, plan_v<Op>(p.V), static_cast<int>(gridDim.x) / CG, C::kGroupM, C::BM);
   const int holder = static_cast<int>(blockIdx.x) / CG;
   const int KB = (p.d + Op::BK - 1) / Op::BK;
@@ -236,9 +305,12 @@ __device__ __forceinline__ void run(uint8_t* smem_raw, const Maps& tm, int count
   if (warp == 0) {
     if (lane == 0) {
       // ------------------------------ TMA producer ------------------------------
+      Turn at;
+#ifdef DLLM_FAULT_SKIP_STAGE
       uint32_t it = 0;
+#endif
       constexpr int kPace = CG == 2 ? DLLM_PAIR_PACE : 0;      // see lm::lmhead_run
-      constexpr int kMates = 40;
+      constexpr int kMates = C::kGroupM;
       int* const progress = p.unit_ctr + ((p.n_cap + 127) / 128 + 2);
       int started = 0;
       int seen[kMates];
@@ -281,36 +353,37 @@ __device__ __forceinline__ void run(uint8_t* smem_raw, const Maps& tm, int count
         const int b_row = n * BN + static_cast<int>(rank) * C::B_ROWS;
         const int valid = count - a_row;
         const int boxes = valid >= C::BM_CTA ? 4 : (valid + 31) / 32;          // CG = 1: valid >= 1
-        for (int kb = 0; kb < KB; ++kb, ++it) {
-          const int s = it % C::kStages;
-          const uint32_t ph = (it / C::kStages) & 1u;
+        for (int kb = 0; kb < KB; ++kb, at.next(sm.stages)) {
+          const int s = at.s;
+          const uint32_t ph = at.ph;
           if (!mbar_wait(smem_u32(&sm.empty[s]), ph ^ 1u, abort_flag, status)) return false;
 #ifdef DLLM_FAULT_SKIP_STAGE
-          if (it == DLLM_FAULT_SKIP_STAGE) continue;
+          // Failure-detection test builds only: this stage is never armed or loaded.
+          if (it++ == DLLM_FAULT_SKIP_STAGE) continue;
 #endif
           const uint32_t fb = smem_u32(&sm.full[s]);
           armed_mask |= 1u << s;
           armed_parity = (armed_parity & ~(1u << s)) | (ph << s);
           // x: elements of the map's type (bf16, bytes of codes, 8-byte words of scales)
           const int x = kb * (Op::kMx4 ? 128 : 64);
-          const uint32_t da = smem_u32(sm.a + s * C::A_BYTES), db = smem_u32(sm.b + s * C::B_BYTES);
+          const uint32_t da = sm.a(s), db = sm.b(s);
           if constexpr (CG == 1) {
-            mbar_arrive_expect_tx(fb, C::STAGE_BYTES - (4 - boxes) * (C::A_BYTES / 4));
+            mbar_arrive_expect_tx(fb, boxes * C::A_BOX + C::B_BYTES + Op::SFA + Op::SFB);
             for (int i = 0; i < boxes; ++i)
-              tma_load_2d(da + i * (C::A_BYTES / 4), tm.a, fb, x, a_row + 32 * i);
+              tma_load_2d(da + i * C::A_BOX, tm.a, fb, x, a_row + 32 * i);
             tma_load_2d(db, tm.b, fb, x, b_row);
             if constexpr (Op::kMx4) {
-              tma_load_2d(smem_u32(sm.sfa + s * Op::SFA), tm.sa, fb, x, a_row / 128);
-              tma_load_2d(smem_u32(sm.sfb + s * Op::SFB), tm.sb, fb, x, n * BN / 128);
+              tma_load_2d(sm.sfa(s), tm.sa, fb, x, a_row / 128);
+              tma_load_2d(sm.sfb(s), tm.sb, fb, x, n * BN / 128);
             }
           } else {
-            if (leader) mbar_arrive_expect_tx(fb, CG * C::STAGE_BYTES);
+            if (leader) mbar_arrive_expect_tx(fb, CG * (4 * C::A_BOX + C::B_BYTES + Op::SFA + Op::SFB));
             const uint32_t fl = fb & kPeerBitMask;
             tma_load_2d_pair(da, tm.a, fl, x, a_row);
             tma_load_2d_pair(db, tm.b, fl, x, b_row);
-            if constexpr (Op::kMx4) {
-              tma_load_2d_pair(smem_u32(sm.sfa + s * Op::SFA), tm.sa, fl, x, a_row / 128);
-              tma_load_2d_pair(smem_u32(sm.sfb + s * Op::SFB), tm.sb, fl, x, n * BN / 128);
+            if constexpr (Op::kMx4) {          // both CTAs of a pair need all of the tile's scales
+              tma_load_2d_pair(sm.sfa(s), tm.sa, fl, x, a_row / 128);
+              tma_load_2d_pair(sm.sfb(s), tm.sb, fl, x, n * BN / 128);
             }
           }
         }
@@ -319,63 +392,95 @@ __device__ __forceinline__ void run(uint8_t* smem_raw, const Maps& tm, int count
       lm::for_each_tile(pl, holder, load_tile);
     }
   } else if (warp == 1) {
-    if (lane == 0 && leader) {
+    if (leader) {
       // ------------------------------ MMA issuer --------------------------------
-      uint32_t it = 0, tile = 0;
+      Turn at, sat, old;          // places in the ring and the scales' ring; the stage whose scale
+      int ahead = 0;              // columns come next
+      uint32_t tile = 0;
       auto mma_tile = [&](int, int n) -> bool {
         const uint32_t buf = tile & 1u, tph = (tile >> 1) & 1u;
-        if (!mbar_wait(smem_u32(&sm.tempty[buf]), tph ^ 1u, abort_flag, status)) return false;
+        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.tempty[buf]), tph ^ 1u, abort_flag, status)))
+          return false;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + buf * BN;
-        for (int kb = 0; kb < KB; ++kb, ++it) {
-          const int s = it % C::kStages;
-          const uint32_t ph = (it / C::kStages) & 1u;
-          if (!mbar_wait(smem_u32(&sm.full[s]), ph, abort_flag, status)) return false;
+        for (int kb = 0; kb < KB; ++kb) {
+          bool got = mbar_wait(smem_u32(&sm.full[at.s]), at.ph, abort_flag, status);
+          if constexpr (Op::kMx4) {
+            if (ahead < Op::kSfRing) {
+              ++ahead;
+            } else {              // the MMAs that read these scale columns are done
+              got = got && mbar_wait(smem_u32(&sm.empty[old.s]), old.ph, abort_flag, status);
+              old.next(sm.stages);
+            }
+          }
+          if (!__all_sync(0xffffffffu, got)) return false;
           tc_fence_after();
-          const uint64_t adesc = sw128_kmajor_desc(smem_u32(sm.a + s * C::A_BYTES));
-          const uint64_t bdesc = sw128_kmajor_desc(smem_u32(sm.b + s * C::B_BYTES));
+          const uint64_t adesc = sw128_kmajor_desc(sm.a(at.s));
+          const uint64_t bdesc = sw128_kmajor_desc(sm.b(at.s));
+          const uint32_t empty = smem_u32(&sm.empty[at.s]);
           if constexpr (!Op::kMx4) {
+            if (elect_one()) {
 #pragma unroll
-            for (int k = 0; k < Op::BK / Op::UK; ++k)
-              lm::mma_issue<CG>(d_tmem, adesc + 2 * k, bdesc + 2 * k, C::kIdesc, (kb | k) != 0 ? 1u : 0u);
+              for (int k = 0; k < Op::BK / Op::UK; ++k)
+                lm::mma_issue<CG>(d_tmem, adesc + 2 * k, bdesc + 2 * k, C::kIdesc, (kb | k) != 0 ? 1u : 0u);
+              lm::mma_commit_all<CG>(empty);            // stage free once these MMAs retire
+            }
           } else {
-            // d is a multiple of 64, so the last stage holds 1 to 4 steps of K = 64; a scale
-            // tile covers two of them (bytes 0, 1 and 2, 3 of its words)
+            // d is a multiple of 64, so the last stage holds 1 to 4 steps of K = 64; a scale tile
+            // covers two of them (bytes 0, 1 and 2, 3 of its words)
             const int left = (p.d - kb * Op::BK) / Op::UK;
-            const int steps = left < 4 ? left : 4;
-            const uint32_t sf = tmem_base + 2 * BN + s * Op::kSfCols;
-            const uint64_t sa = scale_desc(smem_u32(sm.sfa + s * Op::SFA));
-            const uint64_t sb = scale_desc(smem_u32(sm.sfb + s * Op::SFB));
-#pragma unroll
-            for (int g = 0; g < 2; ++g)
-              if (2 * g < steps) {
-                tmem_cp_scales<CG>(sf + 4 * g, sa + 32 * g);              // 512 bytes apart
+            const uint32_t sf = tmem_base + 2 * BN + sat.s * Op::kSfCols;
+            const uint32_t sfb = sf + 8 + ((n * BN) % 128 != 0 ? 2 : 0);
+            const uint64_t sa = scale_desc(sm.sfa(at.s)), sb = scale_desc(sm.sfb(at.s));
+            if (elect_one()) {
+              auto copy = [&](int g) {
+                tmem_cp_scales<CG>(sf + 4 * g, sa + 32 * g);                  // 512 bytes apart
                 tmem_cp_scales<CG>(sf + 8 + 8 * g, sb + 32 * g);
                 tmem_cp_scales<CG>(sf + 8 + 8 * g + 4, sb + 64 + 32 * g);
-              }
-            const uint32_t sfb = sf + 8 + ((n * BN) % 128 != 0 ? 2 : 0);
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (k < steps)
+              };
+              auto mma = [&](int k) {
                 umma_mxf4<CG>(d_tmem, adesc + 2 * k, bdesc + 2 * k,
                               C::kIdesc | ((k & 1) ? (2u << 4) | (2u << 29) : 0u), sf + 4 * (k >> 1),
                               sfb + 8 * (k >> 1), (kb | k) != 0 ? 1u : 0u);
+              };
+              if (left >= 4) {
+                copy(0);
+                copy(1);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) mma(k);
+              } else {
+                copy(0);
+                mma(0);
+                if (left > 1) mma(1);
+                if (left > 2) {
+                  copy(1);
+                  mma(2);
+                }
+              }
+              lm::mma_commit_all<CG>(empty);
+            }
+            sat.next(Op::kSfRing);
           }
-          lm::mma_commit_all<CG>(smem_u32(&sm.empty[s]));
+          __syncwarp();
+          at.next(sm.stages);
         }
-        lm::mma_commit_all<CG>(smem_u32(&sm.tfull[buf]));
+        if (elect_one()) lm::mma_commit_all<CG>(smem_u32(&sm.tfull[buf]));   // accumulator ready
+        __syncwarp();
         ++tile;
         return true;
       };
       if (!lm::for_each_tile(pl, holder, mma_tile)) {
-        lm::mma_commit_all<CG>(smem_u32(sm.drain));       // no MMA may outlive TMEM
-        mbar_wait_drain(smem_u32(sm.drain), 0u, status);
+        if (elect_one()) {
+          lm::mma_commit_all<CG>(smem_u32(sm.drain));       // no MMA may outlive TMEM
+          mbar_wait_drain(smem_u32(sm.drain), 0u, status);
+        }
+        __syncwarp();
       }
     }
-  } else {
+  } else if (warp >= kEpiFirst) {
     // -------------------------------- epilogue ---------------------------------
     const int q = warp & 3;                      // TMEM lane quadrant of this warp
-    const int half = (warp - 2) >> 2;            // which half of a tile's columns
+    const int half = (warp - kEpiFirst) >> 2;            // which half of a tile's columns
     constexpr int kChunks = BN / 64;             // 32-column chunks of a half
     const int row_in_cta = q * 32 + lane;
     const int row_in_tile = static_cast<int>(rank) * C::BM_CTA + row_in_cta;
@@ -469,10 +574,6 @@ __device__ __forceinline__ void run(uint8_t* smem_raw, const Maps& tm, int count
       const auto& c = sm.comb[block * C::BM_CTA + r];
       rules::merge<kExt>(st, c.m, c.s, c.a, c.t, c.m2);
     };
-    auto add_partial = [&](long long e, RowState& st) {
-      rules::merge<kExt>(st, __ldcg(p.part.m + e), __ldcg(p.part.s + e), __ldcg(p.part.a + e),
-                         kExt ? __ldcg(p.part.t + e) : 0.f, kExt ? __ldcg(p.part.m2 + e) : 0.f);
-    };
     // A finished (m-tile, slot): the two halves' states are joined; the result itself when the
     // m-tile has a single unit, else a partial; the last of the m-tile's units to finish merges
     // its rows.
@@ -496,13 +597,8 @@ __device__ __forceinline__ void run(uint8_t* smem_raw, const Maps& tm, int count
       if (half == 0 && valid) {
         const long long e = pl.part_index(g, u.G, slot, m_local * C::BM + row_in_tile);
         if (e < p.part_cap) {
-          p.part.m[e] = st.m;
-          p.part.s[e] = st.s;
-          p.part.a[e] = st.a;
-          if constexpr (kExt) {
-            p.part.t[e] = st.t;
-            p.part.m2[e] = st.m2;
-          }
+          p.part[e] = make_float4(st.m, st.s, st.t, st.m2);
+          p.part_a[e] = st.a;
         } else {
           atomicOr(status, kStatusBounds);             // cannot happen: workspace sized for it
         }
@@ -511,7 +607,7 @@ __device__ __forceinline__ void run(uint8_t* smem_raw, const Maps& tm, int count
       // the partials through L2.
       __threadfence();
       if (!epi_sync()) return false;
-      if (threadIdx.x == 2 * 32) {
+      if (threadIdx.x == kEpiFirst * 32) {
         const int old = atomicAdd(&p.unit_ctr[m_tile * CG + static_cast<int>(rank)], 1);
         *sm.last_flag = old == units - 1 ? 1 : 0;
       }
@@ -522,12 +618,9 @@ __device__ __forceinline__ void run(uint8_t* smem_raw, const Maps& tm, int count
       const int n_valid = count - row0 < C::BM_CTA ? count - row0 : C::BM_CTA;
       const long long base0 = pl.part_index(g, u.G, 0, m_local * C::BM + static_cast<int>(rank) * C::BM_CTA);
       const long long stride = static_cast<long long>(u.G) * C::BM;
-      auto slot_of = [&](int i) { return i < u.P ? i : u.P + j_lo + (i - u.P); };
       if (n_valid <= 32) {
-        for (int r = warp - 2; r < n_valid; r += kEpiWarps) {
-          RowState acc;
-          acc.reset();
-          for (int i = lane; i < units; i += 32) add_partial(base0 + slot_of(i) * stride + r, acc);
+        for (int r = warp - kEpiFirst; r < n_valid; r += kEpiWarps) {
+          RowState acc = merge_slots<kExt>(p.part, p.part_a, base0 + r, stride, lane, units, 32, u.P, j_lo);
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) {
             const float m = __shfl_xor_sync(0xffffffffu, acc.m, o), s = __shfl_xor_sync(0xffffffffu, acc.s, o);
@@ -539,29 +632,19 @@ __device__ __forceinline__ void run(uint8_t* smem_raw, const Maps& tm, int count
           if (lane == 0) write_result(row0 + r, acc);
         }
       } else {
-        // warp quarter q takes the slots [q * units / 4, (q + 1) * units / 4), of the CTA's rows
-        // 64 * half + lane and + 32 more; the quarters meet in shared memory
-        const int s0 = q * units / 4, s1 = (q + 1) * units / 4;
-        RowState acc[2];
-        acc[0].reset();
-        acc[1].reset();
-#pragma unroll 4
-        for (int i = s0; i < s1; ++i) {
-          const long long e = base0 + slot_of(i) * stride + 64 * half + lane;
-          if (64 * half + lane < n_valid) add_partial(e, acc[0]);
-          if (64 * half + lane + 32 < n_valid) add_partial(e + 32, acc[1]);
-        }
-        put(q, 64 * half + lane, acc[0]);
-        put(q, 64 * half + lane + 32, acc[1]);
+        // each warp takes half of the slots, of its own quadrant's rows; the halves meet as above
+        const int mid = units / 2, join = units_done++ & 1;
+        RowState acc;
+        acc.reset();
+        if (valid)
+          acc = merge_slots<kExt>(p.part, p.part_a, base0 + row_in_cta, stride, half ? mid : 0,
+                                  half ? units : mid, 1, u.P, j_lo);
+        if (half == 1) put(join, row_in_cta, acc);
         if (!epi_sync()) return false;
         if (half == 0 && valid) {
-          RowState fin;
-          fin.reset();
-#pragma unroll
-          for (int k = 0; k < 4; ++k) add(k, row_in_cta, fin);
-          write_result(row, fin);
+          add(join, row_in_cta, acc);
+          write_result(row, acc);
         }
-        if (!epi_sync()) return false;           // the blocks are free for the next unit
       }
       return true;
     };
@@ -603,9 +686,9 @@ __device__ __forceinline__ void run(uint8_t* smem_raw, const Maps& tm, int count
     cluster_sync();             // the peer's shared memory stays alive until both have read
   }
   if (aborted) {                // loads already issued land before shared memory is released
-    if (warp == 0 && lane == 0 && (CG == 1 || leader)) {
+    if (warp == 0 && lane == 0 && leader) {
       const unsigned long long deadline = globaltimer_ns() + kWaitLimitNs;
-      for (int s = 0; s < C::kStages; ++s)
+      for (int s = 0; s < sm.stages; ++s)
         if (armed_mask & (1u << s))
           if (!mbar_wait_until(smem_u32(&sm.full[s]), (armed_parity >> s) & 1u, deadline, status)) break;
     }

@@ -609,7 +609,8 @@ dllm_status launch_shaped(const ShapedArgs& x, const DeviceState& ds, const WsLa
   cfg.numAttrs = 2;
   // partials: 16 bytes each in the first four of the workspace's partial arrays (which are one
   // piece), the argmax in the fifth
-  const shaped::Problem p{static_cast<int>(w.rows), a.V, a.d, a.L, a.row_idx,
+  const int tiles = (a.V + Op::BN - 1) / Op::BN;
+  const shaped::Problem p{static_cast<int>(w.rows), a.V, a.d, a.L, shaped::tile_step(tiles), a.row_idx,
                           reinterpret_cast<float4*>(ws + w.pm_off), reinterpret_cast<int*>(ws + w.pm2_off),
                           w.part_cap,
                           reinterpret_cast<int*>(ws + w.ctr_off), outs, ds.status};
@@ -634,6 +635,29 @@ dllm_status launch_shaped(const ShapedArgs& x, const DeviceState& ds, const WsLa
   return cudaPeekAtLastError() == cudaSuccess ? DLLM_OK : DLLM_ERR_CUDA;
 }
 
+// Compaction, and the masked rows of H in MXFP4 into the workspace (prepare_rows for bf16).
+dllm_status prepare_rows_mx4(const LogitsArgs& a, const DeviceState& ds, const WsLayout& w) {
+  const void* Hd = nullptr;
+  const void* Md = nullptr;
+  bool host_rows = false;
+  dllm_status st = resolve_input(a.H, &Hd, &host_rows);
+  if (st != DLLM_OK) return st;
+  if ((st = resolve_input(a.M, &Md)) != DLLM_OK) return st;
+  uint8_t* ws = static_cast<uint8_t*>(a.ws);
+  if ((st = launch_compact(static_cast<const uint8_t*>(Md), a.B, a.L, a.win_lo, a.win_hi, a.row_idx,
+                           a.seq_off, a.count, reinterpret_cast<int*>(ws + w.tiles_off), ds.status,
+                           a.s)) != DLLM_OK)
+    return st;
+  if (launch_pdl(mx4::gather_quantize_kernel, dim3(ds.sms * (host_rows ? DLLM_GATHER_HOST_CTAS : 4)),
+                 dim3(mx4::kThreads), 0, a.s, static_cast<const uint16_t*>(Hd), (const int*)a.row_idx,
+                 (const int*)a.count, static_cast<long long>(a.B) * a.L, w.rows, a.d, ws + w.hm_off,
+                 reinterpret_cast<uint32_t*>(ws + w.hs_off), reinterpret_cast<int*>(ws + w.ctr_off),
+                 w.n_ctr, ds.status) != cudaSuccess)
+    return DLLM_ERR_CUDA;
+  count_launch();
+  return DLLM_OK;
+}
+
 dllm_status run_shaped(const ShapedArgs& x) {
   const LogitsArgs& a = x.a;
   const bool mx4 = x.Wq != nullptr;
@@ -654,27 +678,8 @@ dllm_status run_shaped(const ShapedArgs& x) {
   if (w.rows < 1) return DLLM_ERR_WORKSPACE;
   DeviceState* ds = nullptr;
   if ((st = device_state(&ds)) != DLLM_OK) return st;
-  uint8_t* ws = static_cast<uint8_t*>(a.ws);
-  if (!mx4) {
-    if ((st = prepare_rows(a, *ds, w)) != DLLM_OK) return st;
-  } else {
-    const void* Hd = nullptr;
-    const void* Md = nullptr;
-    bool host_rows = false;
-    if ((st = resolve_input(a.H, &Hd, &host_rows)) != DLLM_OK) return st;
-    if ((st = resolve_input(a.M, &Md)) != DLLM_OK) return st;
-    if ((st = launch_compact(static_cast<const uint8_t*>(Md), a.B, a.L, a.win_lo, a.win_hi, a.row_idx,
-                             a.seq_off, a.count, reinterpret_cast<int*>(ws + w.tiles_off), ds->status,
-                             a.s)) != DLLM_OK)
-      return st;
-    if (launch_pdl(mx4::gather_quantize_kernel, dim3(ds->sms * (host_rows ? DLLM_GATHER_HOST_CTAS : 4)),
-                   dim3(mx4::kThreads), 0, a.s, static_cast<const uint16_t*>(Hd), (const int*)a.row_idx,
-                   (const int*)a.count, static_cast<long long>(a.B) * a.L, w.rows, a.d, ws + w.hm_off,
-                   reinterpret_cast<uint32_t*>(ws + w.hs_off), reinterpret_cast<int*>(ws + w.ctr_off),
-                   w.n_ctr, ds->status) != cudaSuccess)
-      return DLLM_ERR_CUDA;
-    count_launch();
-  }
+  st = mx4 ? prepare_rows_mx4(a, *ds, w) : prepare_rows(a, *ds, w);
+  if (st != DLLM_OK) return st;
   const lm::Outputs outs{a.tok, a.conf, a.lse, a.entropy, a.margin, a.raw, 0};
   return mx4 ? launch_shaped<shaped::Mx4>(x, *ds, w, outs) : launch_shaped<shaped::Bf16>(x, *ds, w, outs);
 }

@@ -96,12 +96,19 @@ __device__ __forceinline__ void prefetch_chunk(int col0, int V, const RowRules& 
 
 // Shape the 32 logits of columns col0 .. col0+31 of each lane's row; what is not allowed, and
 // columns at and past V, become -inf.  Called by all 32 lanes of a warp together: the tests
-// that skip a rule are taken for the warp, whose rows mostly share a sequence.  Returns false
-// if nothing is left in any lane.
-__device__ __forceinline__ bool shape_chunk(float (&v)[32], int col0, int V, const RowRules& r,
-                                            const Words& w) {
-  if (__reduce_or_sync(0xffffffffu, w.ok) == 0u) return false;
+// that skip a rule are taken for the warp, whose rows mostly share a sequence.  The biases are
+// asked for first, then `arrive` waits for the logits themselves.
+template <class Arrive>
+__device__ __forceinline__ void shape_chunk(float (&v)[32], int col0, int V, const RowRules& r,
+                                            const Words& w, Arrive&& arrive) {
   const uint32_t any_seen = __reduce_or_sync(0xffffffffu, w.seen);
+  float4 bias[8];
+  const bool whole = r.bias != nullptr && col0 + 32 <= V;
+  if (whole) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) bias[j] = __ldg(reinterpret_cast<const float4*>(r.bias + col0) + j);
+  }
+  arrive();
   if (any_seen != 0u) {
     // eight columns at a time, without branches: all their counts are asked for before the
     // first is used
@@ -121,28 +128,24 @@ __device__ __forceinline__ bool shape_chunk(float (&v)[32], int col0, int V, con
       }
     }
   }
-  if (r.bias != nullptr) {
-    if (col0 + 32 <= V) {
+  if (whole) {
 #pragma unroll
-      for (int j = 0; j < 32; j += 4) {
-        const float4 b = __ldg(reinterpret_cast<const float4*>(r.bias + col0 + j));
-        v[j + 0] = __fadd_rn(v[j + 0], b.x);
-        v[j + 1] = __fadd_rn(v[j + 1], b.y);
-        v[j + 2] = __fadd_rn(v[j + 2], b.z);
-        v[j + 3] = __fadd_rn(v[j + 3], b.w);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 32; ++j)
-        if (col0 + j < V) v[j] = __fadd_rn(v[j], __ldg(r.bias + col0 + j));
+    for (int j = 0; j < 8; ++j) {
+      v[4 * j + 0] = __fadd_rn(v[4 * j + 0], bias[j].x);
+      v[4 * j + 1] = __fadd_rn(v[4 * j + 1], bias[j].y);
+      v[4 * j + 2] = __fadd_rn(v[4 * j + 2], bias[j].z);
+      v[4 * j + 3] = __fadd_rn(v[4 * j + 3], bias[j].w);
     }
+  } else if (r.bias != nullptr) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (col0 + j < V) v[j] = __fadd_rn(v[j], __ldg(r.bias + col0 + j));
   }
   if (!__all_sync(0xffffffffu, w.ok == 0xffffffffu)) {
 #pragma unroll
     for (int j = 0; j < 32; ++j)
       if (!((w.ok >> j) & 1u)) v[j] = -INFINITY;
   }
-  return true;
 }
 
 // Running statistics of one row, as lm::RowState, with the rounding errors of s and t carried
@@ -179,46 +182,35 @@ __device__ __forceinline__ void kahan(float& sum, float& over, float x) {
 // lm::fold_chunk).
 template <bool kExt>
 __device__ __forceinline__ void fold(const float (&v)[32], int col0, State& st) {
-  float mx, c2 = -INFINITY;                    // the chunk's largest and second largest
-  if constexpr (kExt) {
-    float a[4], b[4];
+  float mx = v[0];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      a[i] = fmaxf(v[2 * i], v[2 * i + 1]);
-      b[i] = fminf(v[2 * i], v[2 * i + 1]);
-    }
-#pragma unroll
-    for (int j = 8; j < 32; ++j) {
-      b[j & 3] = fmaxf(b[j & 3], fminf(a[j & 3], v[j]));
-      a[j & 3] = fmaxf(a[j & 3], v[j]);
-    }
-    const float h0 = fmaxf(a[0], a[1]), l0 = fmaxf(fminf(a[0], a[1]), fmaxf(b[0], b[1]));
-    const float h1 = fmaxf(a[2], a[3]), l1 = fmaxf(fminf(a[2], a[3]), fmaxf(b[2], b[3]));
-    mx = fmaxf(h0, h1);
-    c2 = fmaxf(fminf(h0, h1), fmaxf(l0, l1));
-  } else {
-    mx = v[0];
-#pragma unroll
-    for (int j = 1; j < 32; ++j) mx = fmaxf(mx, v[j]);
-  }
+  for (int j = 1; j < 32; ++j) mx = fmaxf(mx, v[j]);
   if (mx == -INFINITY) return;                 // nothing allowed in this chunk
-  if (mx > st.m) {                             // strict: earlier (lower) index wins ties
+  // of equal maxima the lower token wins; chunks come in any order
+  const bool above = mx > st.m;
+  if (above || (mx == st.m && col0 < st.a)) {
     int j0 = 31;
 #pragma unroll
     for (int j = 31; j >= 0; --j)
       if (v[j] == mx) j0 = j;
-    const float f = ex2_approx((st.m - mx) * lm::kLog2e);
-    if constexpr (kExt) {
-      st.t = f > 0.f ? f * ((st.t - st.tc) + (st.m - mx) * (st.s - st.sc)) : 0.f;
-      st.tc = 0.f;
-      st.m2 = fmaxf(st.m, c2);
-    }
-    st.s *= f;
-    st.sc *= f;
-    st.m = mx;
     st.a = col0 + j0;
-  } else if constexpr (kExt) {
-    st.m2 = fmaxf(st.m2, mx);
+    if (above) {
+      const float f = ex2_approx((st.m - mx) * lm::kLog2e);
+      if constexpr (kExt) {
+        float c2 = -INFINITY;                  // the chunk's second largest (mx again on a tie)
+#pragma unroll
+        for (int j = 0; j < 32; ++j) c2 = fmaxf(c2, j != j0 ? v[j] : -INFINITY);
+        st.t = f > 0.f ? f * ((st.t - st.tc) + (st.m - mx) * (st.s - st.sc)) : 0.f;
+        st.tc = 0.f;
+        st.m2 = fmaxf(st.m, c2);
+      }
+      st.s *= f;
+      st.sc *= f;
+      st.m = mx;
+    }
+  }
+  if constexpr (kExt) {
+    if (!above) st.m2 = fmaxf(st.m2, mx);
   }
   float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f, t0 = 0.f, t1 = 0.f;
 #pragma unroll

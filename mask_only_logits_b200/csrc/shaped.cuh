@@ -21,6 +21,10 @@
 //             comes 2 us after it is asked for when every SM loads).
 //   A rows    single CTAs load their rows of Hm in boxes of 32, only as many as are masked,
 //             and give the rest of the tile's room to more stages.
+//   order     the schedule's vocabulary tile i is tile i * step mod (tiles), step coprime to the
+//             tiles and about 0.62 of them: frequent tokens sit at the low ids of a vocabulary,
+//             so a stream of consecutive tiles would get all the penalised columns (99 us where
+//             the others took 65, 256 rows of d2048 V151936).
 //   epilogue  eight warps: two per TMEM lane quadrant, each with half of a tile's columns (the
 //             rules and scores cost more instructions than the plain statistics, and four MXFP4
 //             tiles take the time of one bf16 tile).  rules::shape_chunk on each 32 logits, then
@@ -100,6 +104,20 @@ __host__ __device__ inline int plan_v(int V) {
   return (V + Op::BN - 1) / Op::BN * lm::BN;
 }
 
+// The step of the walk over the vocabulary tiles: coprime to their number, about 0.62 of it.
+inline int tile_step(int tiles) {
+  int step = static_cast<int>(0.6180339887 * tiles);
+  for (step = step < 1 ? 1 : step;; ++step) {
+    int a = step, b = tiles;
+    while (b != 0) {
+      const int t = a % b;
+      a = b;
+      b = t;
+    }
+    if (a == 1) return step;
+  }
+}
+
 // ---- MXFP4 tensor-core wrappers ---------------------------------------------------------
 // D (+)= (A * scales) * (B * scales)^T, block scaled, 32 elements per scale.
 template <int CG>
@@ -150,7 +168,7 @@ template <int CG, class Op>
 struct Smem {
   using C = Cfg<CG, Op>;
   uint64_t *full, *empty;                            // per stage
-  uint64_t *tfull, *tempty, *drain, *epi_bar;
+  uint64_t *tfull, *tempty, *drain, *epi_bar, *tready;
   uint32_t* tmem_slot;
   int* abort_flag;
   volatile int* last_flag;
@@ -168,7 +186,8 @@ struct Smem {
     tempty = tfull + 2;
     drain = tfull + 4;
     epi_bar = tfull + 5;
-    tmem_slot = reinterpret_cast<uint32_t*>(tfull + 6);
+    tready = tfull + 6;
+    tmem_slot = reinterpret_cast<uint32_t*>(tfull + 7);
     abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
     last_flag = abort_flag + 1;
     comb = reinterpret_cast<RowStateRaw*>(base + kHeadBytes);
@@ -205,6 +224,7 @@ struct Maps {
 
 struct Problem {
   int n_cap, V, d, L;
+  int tile_step;             // order of the vocabulary tiles
   const int* row_idx;
   float4* part;              // per (split, row): m, s, t, m2
   int* part_a;               // and the argmax
@@ -259,48 +279,40 @@ __device__ __forceinline__ void run(uint8_t* smem_raw, const Maps& tm, int count
   const bool leader = rank == 0;
   int* const status = p.status;
 
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < sm.stages; ++s) {
-      mbar_init(smem_u32(&sm.full[s]), 1);
-      mbar_init(smem_u32(&sm.empty[s]), 1);
-    }
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(smem_u32(&sm.tfull[b]), 1);
-      mbar_init(smem_u32(&sm.tempty[b]), CG * kEpiWarps);
-    }
-    mbar_init(smem_u32(sm.drain), 1);
-    mbar_init(smem_u32(sm.epi_bar), kEpiWarps);
-    *sm.abort_flag = 0;
-    fence_mbar_init();
-  }
-  if (warp == 0 && lane == 0) {
-    tma_prefetch_desc(tm.a);
-    tma_prefetch_desc(tm.b);
-    if constexpr (Op::kMx4) {
-      tma_prefetch_desc(tm.sa);
-      tma_prefetch_desc(tm.sb);
-    }
-  }
+  // TMEM, while the first loads are on their way; tready: both CTAs of a pair have theirs
   if (warp == 1) {
     if constexpr (CG == 1) {
       tmem_alloc(smem_u32(sm.tmem_slot), 512);
       tmem_relinquish();
+      tc_fence_before();
+      if (lane < 2) mbar_arrive(smem_u32(sm.tready));
     } else {
       tmem_alloc_pair(smem_u32(sm.tmem_slot), 512);
       tmem_relinquish_pair();
+      tc_fence_before();
+      if (lane < 2) mbar_arrive_cluster(smem_u32(sm.tready), lane);
     }
+    __syncwarp();
   }
-  tc_fence_before();
-  if constexpr (CG == 1) __syncthreads();
-  else cluster_sync();          // barriers of both CTAs initialised before any remote use
-  tc_fence_after();
-  const uint32_t tmem_base = __shfl_sync(0xffffffffu, *sm.tmem_slot, 0);
   volatile int* abort_flag = sm.abort_flag;
 
   const Plan pl = Plan::make(count, plan_v<Op>(p.V), static_cast<int>(gridDim.x) / CG, C::kGroupM, C::BM);
   const int holder = static_cast<int>(blockIdx.x) / CG;
   const int KB = (p.d + Op::BK - 1) / Op::BK;
+  // the schedule's vocabulary tile i, in the order of the walk
+  auto tile_at = [&](int i) {
+    const unsigned n = static_cast<unsigned>(pl.numN), u = static_cast<unsigned>(i), v = static_cast<unsigned>(p.tile_step);
+    return static_cast<int>(n < 65536u ? u * v % n : static_cast<unsigned>(static_cast<unsigned long long>(u) * v % n));
+  };
   uint32_t armed_mask = 0, armed_parity = 0;      // as in lm::lmhead_run
+  // TMEM's base address once it is allocated; false if the CTA is aborting
+  uint32_t tmem_base = 0;
+  auto wait_tmem = [&]() -> bool {
+    const bool got = __all_sync(0xffffffffu, mbar_wait(smem_u32(sm.tready), 0u, abort_flag, status));
+    tc_fence_after();
+    tmem_base = __shfl_sync(0xffffffffu, *sm.tmem_slot, 0);
+    return got;
+  };
 
   if (warp == 0) {
     if (lane == 0) {
@@ -346,8 +358,9 @@ __device__ __forceinline__ void run(uint8_t* smem_raw, const Maps& tm, int count
           if (j < pl.gmax) seen[j] = ld_relaxed_gpu(progress + first + j);
         return true;
       };
-      auto load_tile = [&](int m_tile, int n) -> bool {
+      auto load_tile = [&](int m_tile, int i) -> bool {
         if (!pace(m_tile)) return false;
+        const int n = tile_at(i);
         ++started;
         const int a_row = m_tile * C::BM + static_cast<int>(rank) * C::BM_CTA;
         const int b_row = n * BN + static_cast<int>(rank) * C::B_ROWS;
@@ -369,8 +382,8 @@ __device__ __forceinline__ void run(uint8_t* smem_raw, const Maps& tm, int count
           const uint32_t da = sm.a(s), db = sm.b(s);
           if constexpr (CG == 1) {
             mbar_arrive_expect_tx(fb, boxes * C::A_BOX + C::B_BYTES + Op::SFA + Op::SFB);
-            for (int i = 0; i < boxes; ++i)
-              tma_load_2d(da + i * C::A_BOX, tm.a, fb, x, a_row + 32 * i);
+            for (int j = 0; j < boxes; ++j)
+              tma_load_2d(da + j * C::A_BOX, tm.a, fb, x, a_row + 32 * j);
             tma_load_2d(db, tm.b, fb, x, b_row);
             if constexpr (Op::kMx4) {
               tma_load_2d(sm.sfa(s), tm.sa, fb, x, a_row / 128);
@@ -397,7 +410,8 @@ __device__ __forceinline__ void run(uint8_t* smem_raw, const Maps& tm, int count
       Turn at, sat, old;          // places in the ring and the scales' ring; the stage whose scale
       int ahead = 0;              // columns come next
       uint32_t tile = 0;
-      auto mma_tile = [&](int, int n) -> bool {
+      auto mma_tile = [&](int, int i) -> bool {
+        const int n = tile_at(i);
         const uint32_t buf = tile & 1u, tph = (tile >> 1) & 1u;
         if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.tempty[buf]), tph ^ 1u, abort_flag, status)))
           return false;
@@ -469,7 +483,7 @@ __device__ __forceinline__ void run(uint8_t* smem_raw, const Maps& tm, int count
         ++tile;
         return true;
       };
-      if (!lm::for_each_tile(pl, holder, mma_tile)) {
+      if (!wait_tmem() || !lm::for_each_tile(pl, holder, mma_tile)) {
         if (elect_one()) {
           lm::mma_commit_all<CG>(smem_u32(sm.drain));       // no MMA may outlive TMEM
           mbar_wait_drain(smem_u32(sm.drain), 0u, status);
@@ -484,9 +498,10 @@ __device__ __forceinline__ void run(uint8_t* smem_raw, const Maps& tm, int count
     constexpr int kChunks = BN / 64;             // 32-column chunks of a half
     const int row_in_cta = q * 32 + lane;
     const int row_in_tile = static_cast<int>(rank) * C::BM_CTA + row_in_cta;
+    bool ok = wait_tmem();
     const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + half * (BN / 2);
     uint32_t tile = 0, epi_phase = 0, units_done = 0;
-    bool ok = true, live = false;                // live: this warp holds a masked row of the m-tile
+    bool live = false;                // live: this warp holds a masked row of the m-tile
     rules::RowRules rr = rules::no_rules();
     auto enter_m_tile = [&](int m_tile) {
       live = m_tile * C::BM + row_in_tile - lane < count;
@@ -508,9 +523,9 @@ __device__ __forceinline__ void run(uint8_t* smem_raw, const Maps& tm, int count
     auto consume = [&](int n, rules::State& st) -> bool {
       const uint32_t buf = tile & 1u, tph = (tile >> 1) & 1u;
       const int first = n * BN + half * (BN / 2);
+      rules::Words w[kChunks];
       if constexpr (kRules) {
         if (live) {
-          rules::Words w[kChunks];
 #pragma unroll
           for (int c = 0; c < kChunks; ++c) w[c] = rules::load_words(first + 32 * c, p.V, rr);
 #pragma unroll
@@ -526,16 +541,23 @@ __device__ __forceinline__ void run(uint8_t* smem_raw, const Maps& tm, int count
         for (int c = 0; c < kChunks; ++c) {
           float v[32];
           const int col0 = first + c * 32;
-          rules::Words w;
-          if constexpr (kRules) w = rules::load_words(col0, p.V, rr);
           tmem_ld32(taddr + c * 32, v);
-          tmem_ld_wait();
           if constexpr (kRules) {
-            if (!rules::shape_chunk(v, col0, p.V, rr, w)) continue;
-          } else if (col0 + 32 > p.V) {
+            const rules::Words wc = w[0];
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (col0 + j >= p.V) v[j] = -INFINITY;
+            for (int k = 1; k < kChunks; ++k) w[k - 1] = w[k];       // the next chunk's words
+            if (__reduce_or_sync(0xffffffffu, wc.ok) == 0u) {
+              tmem_ld_wait();
+              continue;
+            }
+            rules::shape_chunk(v, col0, p.V, rr, wc, [] { tmem_ld_wait(); });
+          } else {
+            tmem_ld_wait();
+            if (col0 + 32 > p.V) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (col0 + j >= p.V) v[j] = -INFINITY;
+            }
           }
           rules::fold<kExt>(v, col0, st);
         }
@@ -544,9 +566,9 @@ __device__ __forceinline__ void run(uint8_t* smem_raw, const Maps& tm, int count
       __syncwarp();
       // release the accumulator: the leader's MMA waits for the epilogues of both CTAs
       if (lane == 0) {
-        if constexpr (CG == 1) mbar_arrive(smem_u32(&sm.tempty[buf]));
-        else mbar_arrive_cluster(smem_u32(&sm.tempty[buf]), 0u);
+        if constexpr (CG == 2) mbar_arrive_cluster(smem_u32(&sm.tempty[buf]), 0u);
       }
+      if (CG == 1 && lane < 2) mbar_arrive(smem_u32(&sm.tempty[buf]));    // twice: it counts both variants
       ++tile;
       return true;
     };
@@ -603,17 +625,17 @@ __device__ __forceinline__ void run(uint8_t* smem_raw, const Maps& tm, int count
           atomicOr(status, kStatusBounds);             // cannot happen: workspace sized for it
         }
       }
-      // Writers fence before the counter increment; the last arriver fences after it and reads
-      // the partials through L2.
-      __threadfence();
+      // Once all partials are written, one thread fences (for the whole CTA: its fence follows the
+      // meeting), counts the unit and fences again; the last unit's CTA reads through L2.
       if (!epi_sync()) return false;
       if (threadIdx.x == kEpiFirst * 32) {
+        __threadfence();
         const int old = atomicAdd(&p.unit_ctr[m_tile * CG + static_cast<int>(rank)], 1);
+        __threadfence();
         *sm.last_flag = old == units - 1 ? 1 : 0;
       }
       if (!epi_sync()) return false;
       if (!*sm.last_flag) return true;
-      __threadfence();
       const int row0 = m_tile * C::BM + static_cast<int>(rank) * C::BM_CTA;   // CTA's first row
       const int n_valid = count - row0 < C::BM_CTA ? count - row0 : C::BM_CTA;
       const long long base0 = pl.part_index(g, u.G, 0, m_local * C::BM + static_cast<int>(rank) * C::BM_CTA);
@@ -652,27 +674,29 @@ __device__ __forceinline__ void run(uint8_t* smem_raw, const Maps& tm, int count
     for (int g = 0; g < pl.ngroups && ok; ++g) {
       Unit u;
       if (!lm::unit_of(pl, g, holder, u)) continue;
+      // a stream's tiles, or remainder tiles in m-major order: one running state, finished where
+      // the m-tile changes
+      const int n_tiles = u.leftover ? static_cast<int>(u.i1 - u.i0) : u.n1 - u.n0;
       rules::State st;
-      st.reset();
-      if (u.leftover) {
-        int cur = -1;
-        for (long long i = u.i0; i < u.i1 && ok; ++i) {
-          const int m_local = static_cast<int>(i / pl.rr);
-          const int n = u.P * pl.rb + static_cast<int>(i % pl.rr);
-          if (m_local != cur) {
-            if (cur >= 0) ok = finish(g, u, cur, u.p, st);
-            cur = m_local;
-            st.reset();
-            enter_m_tile(g * pl.gmax + m_local);
-          }
-          if (ok && !consume(n, st)) ok = false;
+      int m_local = u.leftover ? static_cast<int>(u.i0 / pl.rr) : u.m_local;
+      bool fresh = true;
+      for (int j = 0; j < n_tiles && ok; ++j) {
+        int i = u.n0 + j, next_m = m_local;
+        if (u.leftover) {
+          i = u.P * pl.rb + static_cast<int>((u.i0 + j) % pl.rr);
+          next_m = static_cast<int>((u.i0 + j + 1) / pl.rr);
         }
-        if (ok && cur >= 0) ok = finish(g, u, cur, u.p, st);
-      } else {
-        enter_m_tile(u.m_tile);
-        for (int n = u.n0; n < u.n1 && ok; ++n)
-          if (!consume(n, st)) ok = false;
-        if (ok) ok = finish(g, u, u.m_local, u.p, st);
+        if (fresh) {
+          st.reset();
+          enter_m_tile(g * pl.gmax + m_local);
+          fresh = false;
+        }
+        ok = consume(tile_at(i), st);
+        if (ok && (j + 1 == n_tiles || next_m != m_local)) {
+          ok = finish(g, u, m_local, u.p, st);
+          m_local = next_m;
+          fresh = true;
+        }
       }
     }
   }
@@ -698,6 +722,7 @@ __device__ __forceinline__ void run(uint8_t* smem_raw, const Maps& tm, int count
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
+    tmem_base = __shfl_sync(0xffffffffu, *sm.tmem_slot, 0);
     if constexpr (CG == 1) tmem_dealloc(tmem_base, 512);
     else tmem_dealloc_pair(tmem_base, 512);
   }
@@ -713,6 +738,33 @@ shaped_kernel(const __grid_constant__ CUtensorMap tmA1, const __grid_constant__ 
               const int* __restrict__ count_ptr, int variant, const Problem p,
               const __grid_constant__ dllm_logit_rules rule_set) {
   extern __shared__ uint8_t smem_raw[];
+  // What no variant changes is set up while the staging kernel still runs.
+  const Smem<1, Op> sm(smem_raw, 1);
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kMaxStages; ++s) {
+      mbar_init(smem_u32(&sm.full[s]), 1);
+      mbar_init(smem_u32(&sm.empty[s]), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(smem_u32(&sm.tfull[b]), 1);
+      mbar_init(smem_u32(&sm.tempty[b]), 2 * kEpiWarps);
+    }
+    mbar_init(smem_u32(sm.drain), 1);
+    mbar_init(smem_u32(sm.epi_bar), kEpiWarps);
+    mbar_init(smem_u32(sm.tready), 2);
+    *sm.abort_flag = 0;
+    fence_mbar_init();
+  } else if (threadIdx.x == 32) {
+    tma_prefetch_desc(&tmA1);
+    tma_prefetch_desc(&tmA2);
+    tma_prefetch_desc(&tmB1);
+    tma_prefetch_desc(&tmB2);
+    if constexpr (Op::kMx4) {
+      tma_prefetch_desc(&tmSA);
+      tma_prefetch_desc(&tmSB);
+    }
+  }
+  cluster_sync();               // barriers of both CTAs initialised before any remote use
   pdl_wait();
   pdl_launch_dependents();
   const int c = *count_ptr;

@@ -275,6 +275,7 @@ def test_rows(dl, case, mx4, variant):
         dl.debug_set_gemm_variant(0)
     assert int(o["count"][0]) == c
     np.testing.assert_array_equal(o["row_idx"][:c].cpu().numpy(), r["pos"])
+    np.testing.assert_array_equal(o["seq_off"].cpu().numpy(), np.searchsorted(r["pos"], np.arange(B + 1) * L))
     check(o, r, V, ext)
     for k in ("tok", "conf", "lse", "entropy", "margin", "row_idx"):       # rows behind the last
         if o[k] is not None:
@@ -294,6 +295,29 @@ def test_mx4_without_rules(dl, shape, ext):
     check(o, r, V, ext)
     # sums of a few bits each: the first of equal maxima, exactly
     np.testing.assert_array_equal(o["tok"].cpu().numpy(), r["tok"])
+
+
+@pytest.mark.parametrize("mx4", [False, True], ids=["bf16", "mx4"])
+def test_mask_of_many_positions(dl, mx4):
+    """More positions than one launch stages (65536), and exactly as many: the same rows."""
+    d, V = 64, 300
+    for B, L in ((2, 32768), (3, 21846)):
+        H, M, W = head_inputs(B, L, d, V, "none", seed=9)
+        pos = np.sort(np.random.default_rng(1).choice(B * L, 200, replace=False))
+        M.view(-1)[pos] = 1
+        M[B - 1, L - 1] = 1
+        pos = np.flatnonzero(M.numpy().reshape(-1))
+        ref_rules, dev = make_rules(["penalty", "grammar"], B, L, V, seed=1)
+        r = reference(H, M, W, mx4, ref_rules, pos)
+        o = outputs(B * L, B, ALL)
+        ws = torch.empty((dl.workspace_bytes_mx4 if mx4 else dl.workspace_bytes_rows)(B, L, d, V, 300),
+                         dtype=torch.uint8, device="cuda")
+        call(dl, mx4, H.cuda(), M.cuda(), dl.Mx4Matrix.quantize(W.cuda()) if mx4 else W.cuda(),
+             dl.LogitRules(B, L, V, **dev), ALL, o, ws)
+        assert dl.get_status() == 0 and int(o["count"][0]) == len(pos)
+        check(o, r, V, ALL)
+        np.testing.assert_array_equal(o["row_idx"][:len(pos)].cpu().numpy(), pos)
+        np.testing.assert_array_equal(o["seq_off"].cpu().numpy(), np.searchsorted(pos, np.arange(B + 1) * L))
 
 
 @pytest.mark.parametrize("mx4", [False, True], ids=["bf16", "mx4"])
@@ -350,6 +374,43 @@ def test_lowest_value_everywhere(dl, mx4):
     np.testing.assert_allclose(o["conf"].cpu().numpy(), 1 / V, rtol=2.0 ** -22)
     np.testing.assert_allclose(o["entropy"].cpu().numpy(), np.log(V), rtol=2.0 ** -21)
     assert (o["margin"] == 0).all() and (o["lse"] == torch.finfo(torch.float32).min).all()
+
+
+@pytest.mark.parametrize("variant", [0, 1, 2], ids=["auto", "single", "pair"])
+@pytest.mark.parametrize("mx4", [False, True], ids=["bf16", "mx4"])
+def test_first_of_equal_maxima(dl, mx4, variant):
+    """Equal logits in tiles that different CTAs, and one CTA in any order, walk over: the lowest
+    allowed token wins.  Row l's largest logit stands at five tokens; where all are equal the
+    first token does."""
+    B, L, d, V = 1, 130, 64, 90001
+    rng = np.random.default_rng(0)
+    W = torch.zeros(V, d, dtype=torch.bfloat16)
+    H = torch.zeros(L, d, dtype=torch.bfloat16)
+    want = np.zeros(L, dtype=np.int64)
+    allow = np.ones((L, V), dtype=bool)
+    for l in range(L - 2):                           # the last two rows are zero: all logits equal
+        H[l, l % d] = 2.0 if l < d else -2.0
+        if l < d:
+            at = np.sort(rng.choice(V, 10, replace=False))
+            W[at[:5], l], W[at[5:], l] = 4.0, -4.0   # rows l and l + d: the same column, two signs
+        at = np.flatnonzero(W[:, l % d].float().numpy() == (4.0 if l < d else -4.0))
+        allow[l, at[0]] = l % 3 != 0                 # some rows may not take the first of them
+        want[l] = at[0] if allow[l, at[0]] else at[1]
+    rules = dl.LogitRules(B, L, V, allow=torch.from_numpy(S.pack_bits(allow)).cuda(),
+                          allow_id=torch.arange(L, dtype=torch.int32, device="cuda")[None])
+    M = torch.ones(B, L, dtype=torch.uint8, device="cuda")
+    ws = torch.empty(max(dl.workspace_bytes(B, L, d, V), dl.workspace_bytes_mx4(B, L, d, V)),
+                     dtype=torch.uint8, device="cuda")
+    Wd = dl.Mx4Matrix.quantize(W.cuda()) if mx4 else W.cuda()
+    o = outputs(L, B, ALL)
+    dl.debug_set_gemm_variant(variant)
+    try:
+        call(dl, mx4, H.cuda(), M, Wd, rules, ALL, o, ws)
+        assert dl.get_status() == 0
+    finally:
+        dl.debug_set_gemm_variant(0)
+    np.testing.assert_array_equal(o["tok"].cpu().numpy(), want)
+    assert (o["margin"] == 0).all()
 
 
 def test_bitmap_number_out_of_range_is_recorded(dl):

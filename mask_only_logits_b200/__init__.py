@@ -417,15 +417,38 @@ def _bitmap_words(V: int) -> int:
     return (V + 31) // 32
 
 
-def _same_device(**tensors) -> None:
-    """The library launches on the current device: every CUDA tensor must live there."""
-    cur = None
-    for name, t in tensors.items():
-        if t is not None and t.is_cuda:
-            if cur is None:
-                cur = torch.cuda.current_device()
-            if t.device.index != cur:
-                raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{cur}")
+def _call_device(t: torch.Tensor) -> int:
+    """Device number of a call whose output is t: the library launches on the current device,
+    so a tensor of another one is refused.  -2 (no device's number) for a CPU tensor: every
+    argument then goes through the single checks, which name what is wrong."""
+    dev = t.get_device()
+    if dev < 0:
+        return -2
+    cur = torch.cuda.current_device()
+    if dev != cur:
+        raise ValueError(f"tensors on cuda:{dev}, but the current device is cuda:{cur}")
+    return dev
+
+
+def _stream_on(stream, dev: int):
+    """_stream for a call on device `dev`: the current stream's handle without building its
+    Python object (3 us of a 10 us call)."""
+    if stream is None and dev >= 0:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return _stream(stream)
+
+
+def _arg(t: torch.Tensor | None, dtype: torch.dtype, name: str, n: int, dev: int,
+         host_ok: bool = False):
+    """Pointer argument of a call on device `dev`: _ptr's checks and the device, in one go where
+    all is well."""
+    if t is None:
+        return None
+    if (t.dtype is dtype and t.get_device() == dev and t.numel() >= n and t.is_contiguous()):
+        return t.data_ptr()
+    if t.is_cuda and t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, but the call runs on cuda:{dev}")
+    return _ptr(t, dtype, name, host_ok, n)
 
 
 def _rows_ptr(t, dtypes, name: str, rows: int, cols: int) -> tuple:
@@ -501,12 +524,15 @@ class LogitRules:
             elif allow.shape[0] not in (1, B):
                 raise ValueError(f"allow: {allow.shape[0]} bitmaps for {B} sequences need allow_id")
         self._struct = r
+        self._devices = {t.get_device() for t in self.tensors.values() if t is not None}
 
-    def _ref(self, B: int, L: int, V: int):
-        if (B, L, V) != (self.B, self.L, self.V):
+    def _ref(self, B: int, L: int, V: int, dev: int):
+        if B != self.B or L != self.L or V != self.V:
             raise ValueError(f"rules: made for (B, L, V) = {(self.B, self.L, self.V)}, "
                              f"used with {(B, L, V)}")
-        _same_device(**self.tensors)
+        if dev >= 0 and not self._devices <= {dev}:
+            raise ValueError(f"rules: tensors on devices {sorted(self._devices)}, "
+                             f"but the call runs on cuda:{dev}")
         return ctypes.byref(self._struct)
 
 
@@ -523,28 +549,28 @@ def token_counts(tokens, counts, seen, M=None, n_valid=None, accumulate=False, s
                          f"{list(counts.shape)} and {list(seen.shape)}")
     if seen.dtype not in (torch.int32, torch.uint32):
         raise ValueError(f"seen: expected torch.int32, got {seen.dtype}")
-    _same_device(tokens=tokens, counts=counts, seen=seen, M=M, n_valid=n_valid)
+    dev = _call_device(counts)
     _check(lib().dllm_token_counts(
-        _ptr(tokens, torch.int32, "tokens"), _ptr(M, torch.uint8, "M", n=B * n),
-        _ptr(n_valid, torch.int32, "n_valid", n=B), B, n, V, 1 if accumulate else 0,
-        _ptr(counts, torch.int32, "counts"), _ptr(seen, None, "seen"), _stream(stream)),
-        "dllm_token_counts")
+        _arg(tokens, torch.int32, "tokens", 0, dev), _arg(M, torch.uint8, "M", B * n, dev),
+        _arg(n_valid, torch.int32, "n_valid", B, dev), B, n, V, 1 if accumulate else 0,
+        _arg(counts, torch.int32, "counts", B * V, dev), _arg(seen, seen.dtype, "seen", 0, dev),
+        _stream_on(stream, dev)), "dllm_token_counts")
 
 
-def _shaped_args(H, M, stats, tok, conf, lse, entropy, margin, row_idx, seq_off, count, ws,
-                 win_lo, win_hi, d: int) -> tuple:
+def _logits_args(H, M, d, tok, conf, lse, entropy, margin, row_idx, seq_off, count, ws, win_lo,
+                 win_hi, dev: int) -> tuple:
     """(pointers of H and M; of the windows; of the outputs, workspace and its size)."""
     B, L = M.shape
-    n = B * L
-    _same_device(H=H, M=M, tok=tok, conf=conf, lse=lse, entropy=entropy, margin=margin,
-                 row_idx=row_idx, seq_off=seq_off, count=count, ws=ws, win_lo=win_lo, win_hi=win_hi)
-    return ((_ptr(H, torch.bfloat16, "H", True, n * d), _ptr(M, torch.uint8, "M", True)),
-            (_ptr(win_lo, torch.int32, "win_lo", n=B), _ptr(win_hi, torch.int32, "win_hi", n=B)),
-            (_ptr(tok, torch.int32, "tok", n=n), _ptr(conf, torch.float32, "conf", n=n),
-             _ptr(lse, torch.float32, "lse", n=n), _ptr(entropy, torch.float32, "entropy", n=n),
-             _ptr(margin, torch.float32, "margin", n=n), _ptr(row_idx, torch.int32, "row_idx", n=n),
-             _ptr(seq_off, torch.int32, "seq_off", n=B + 1), _ptr(count, torch.int32, "count", n=1),
-             _ptr(ws, None, "ws"), ws.numel() * ws.element_size()))
+    n, i32, f32 = B * L, torch.int32, torch.float32
+    no_win = win_lo is None and win_hi is None
+    return ((_arg(H, torch.bfloat16, "H", n * d, dev, True), _arg(M, torch.uint8, "M", n, dev, True)),
+            (None, None) if no_win else (_arg(win_lo, i32, "win_lo", B, dev),
+                                         _arg(win_hi, i32, "win_hi", B, dev)),
+            (_arg(tok, i32, "tok", n, dev), _arg(conf, f32, "conf", n, dev), _arg(lse, f32, "lse", n, dev),
+             _arg(entropy, f32, "entropy", n, dev), _arg(margin, f32, "margin", n, dev),
+             _arg(row_idx, i32, "row_idx", n, dev), _arg(seq_off, i32, "seq_off", B + 1, dev),
+             _arg(count, i32, "count", 1, dev), _arg(ws, ws.dtype, "ws", 0, dev),
+             ws.numel() * ws.element_size()))
 
 
 def masked_logits_rules(H, M, W, rules: LogitRules, stats, tok, conf, lse, entropy, margin, row_idx,
@@ -553,11 +579,11 @@ def masked_logits_rules(H, M, W, rules: LogitRules, stats, tok, conf, lse, entro
     token left gets tok -1, conf 0, lse -inf, entropy +inf, margin 0."""
     B, L = M.shape
     V, d = W.shape
-    _same_device(W=W)
-    ins, win, outs = _shaped_args(H, M, stats, tok, conf, lse, entropy, margin, row_idx, seq_off,
-                                  count, ws, win_lo, win_hi, d)
-    _check(lib().dllm_masked_logits_rules(*ins, _ptr(W, torch.bfloat16, "W"), B, L, d, V, *win,
-                                          rules._ref(B, L, V), stats, *outs, _stream(stream)),
+    dev = _call_device(count)
+    ins, win, outs = _logits_args(H, M, d, tok, conf, lse, entropy, margin, row_idx, seq_off, count,
+                                  ws, win_lo, win_hi, dev)
+    _check(lib().dllm_masked_logits_rules(*ins, _arg(W, torch.bfloat16, "W", 0, dev), B, L, d, V, *win,
+                                          rules._ref(B, L, V, dev), stats, *outs, _stream_on(stream, dev)),
            "dllm_masked_logits_rules")
 
 
@@ -569,30 +595,32 @@ def mx4_scale_bytes(rows: int, cols: int) -> int:
     return int(lib().dllm_mx4_scale_bytes(rows, cols))
 
 
-def _mx4_args(X, q, s, dtypes) -> tuple:
+def _mx4_args(X, q, s, dtypes, stream) -> tuple:
     rows, cols = X.shape
     if cols % 32 != 0 or cols == 0:
         raise ValueError(f"X: {cols} columns are not a positive multiple of 32")
     ptr, ld = _rows_ptr(X, dtypes, "X", rows, cols)
-    _same_device(X=X, q=q, s=s)
-    return (ctypes.c_void_p(ptr), _MX4_DTYPES[X.dtype], rows, cols, ld,
-            _ptr(q, torch.uint8, "q", n=rows * (cols // 2)),
-            _ptr(s, torch.uint8, "s", n=-(-rows // 128) * -(-cols // 128) * 512))
+    dev = _call_device(X)
+    return (ptr, _MX4_DTYPES[X.dtype], rows, cols, ld,
+            _arg(q, torch.uint8, "q", rows * (cols // 2), dev),
+            _arg(s, torch.uint8, "s", -(-rows // 128) * -(-cols // 128) * 512, dev),
+            _stream_on(stream, dev))
 
 
 def mx4_quantize(X, q, s, stream=None) -> None:
     """X [rows, cols] (bf16, fp16 or fp32; rows may be strided) to MXFP4: codes q uint8
     [rows, cols / 2] and scales s uint8 [mx4_scale_bytes(rows, cols)]."""
-    ptr, dt, rows, cols, ld, qp, sp = _mx4_args(X, q, s, (torch.bfloat16, torch.float16, torch.float32))
-    _check(lib().dllm_mx4_quantize(ptr, dt, rows, cols, ld, qp, sp, _stream(stream)),
+    ptr, dt, rows, cols, ld, qp, sp, st = _mx4_args(
+        X, q, s, (torch.bfloat16, torch.float16, torch.float32), stream)
+    _check(lib().dllm_mx4_quantize(ptr, dt, rows, cols, ld, qp, sp, st),
            "dllm_mx4_quantize")
 
 
 def mx4_dequantize(q, s, X, stream=None) -> None:
     """The values that codes q and scales s stand for, into X [rows, cols] (bf16 or fp32, both
     exact)."""
-    ptr, dt, rows, cols, ld, qp, sp = _mx4_args(X, q, s, (torch.bfloat16, torch.float32))
-    _check(lib().dllm_mx4_dequantize(qp, sp, rows, cols, dt, ptr, ld, _stream(stream)),
+    ptr, dt, rows, cols, ld, qp, sp, st = _mx4_args(X, q, s, (torch.bfloat16, torch.float32), stream)
+    _check(lib().dllm_mx4_dequantize(qp, sp, rows, cols, dt, ptr, ld, st),
            "dllm_mx4_dequantize")
 
 
@@ -664,12 +692,12 @@ def masked_logits_mx4(H, M, W: Mx4Matrix, rules: LogitRules | None, stats, tok, 
     logits if given.  ws: workspace_bytes_mx4 bytes."""
     B, L = M.shape
     V, d = W.shape
-    _same_device(Wq=W.q, Ws=W.s)
-    ins, win, outs = _shaped_args(H, M, stats, tok, conf, lse, entropy, margin, row_idx, seq_off,
-                                  count, ws, win_lo, win_hi, d)
+    dev = _call_device(count)
+    ins, win, outs = _logits_args(H, M, d, tok, conf, lse, entropy, margin, row_idx, seq_off, count,
+                                  ws, win_lo, win_hi, dev)
     _check(lib().dllm_masked_logits_mx4(
-        *ins, _ptr(W.q, torch.uint8, "Wq"), _ptr(W.s, torch.uint8, "Ws"), B, L, d, V, *win,
-        None if rules is None else rules._ref(B, L, V), stats, *outs, _stream(stream)),
+        *ins, _arg(W.q, torch.uint8, "Wq", 0, dev), _arg(W.s, torch.uint8, "Ws", 0, dev), B, L, d, V,
+        *win, None if rules is None else rules._ref(B, L, V, dev), stats, *outs, _stream_on(stream, dev)),
         "dllm_masked_logits_mx4")
 
 

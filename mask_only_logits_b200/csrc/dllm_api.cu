@@ -1170,8 +1170,7 @@ dllm_status dllm_mx4_quantize(const void* X, int32_t dtype, int64_t rows, int32_
   if (st != DLLM_OK) return st;
   DeviceState* ds = nullptr;
   if ((st = device_state(&ds)) != DLLM_OK) return st;
-  const long long blocks = (rows + 127) / 128 * 128 * ((cols + 127) / 128 * 4);
-  const dim3 grid(grid_for(blocks, mx4::kThreads, ds->sms * 16ll)), thr(mx4::kThreads);
+  const dim3 grid(grid_for((rows + 127) / 128 * 128, mx4::kThreads / 32, static_cast<long long>(ds->sms) * mx4::kGridPerSm)), thr(mx4::kThreads);
   uint32_t* sw = reinterpret_cast<uint32_t*>(s);
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
   cudaError_t e;
@@ -1196,12 +1195,13 @@ dllm_status dllm_mx4_dequantize(const uint8_t* q, const uint8_t* s, int64_t rows
   if (st != DLLM_OK) return st;
   DeviceState* ds = nullptr;
   if ((st = device_state(&ds)) != DLLM_OK) return st;
-  const dim3 grid(grid_for(rows * (cols / 8), mx4::kThreads, ds->sms * 16ll)), thr(mx4::kThreads);
+  const dim3 grid(grid_for(rows, mx4::kThreads / 32, static_cast<long long>(ds->sms) * mx4::kGridPerSm)), thr(mx4::kThreads);
+  const uint32_t* sw = reinterpret_cast<const uint32_t*>(s);
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
   const cudaError_t e = dtype == DLLM_BF16
-      ? launch_pdl(mx4::dequantize_kernel<__nv_bfloat16>, grid, thr, 0, cs, q, s, (long long)rows, cols,
+      ? launch_pdl(mx4::dequantize_kernel<__nv_bfloat16>, grid, thr, 0, cs, q, sw, (long long)rows, cols,
                    static_cast<__nv_bfloat16*>(X), (long long)ld)
-      : launch_pdl(mx4::dequantize_kernel<float>, grid, thr, 0, cs, q, s, (long long)rows, cols,
+      : launch_pdl(mx4::dequantize_kernel<float>, grid, thr, 0, cs, q, sw, (long long)rows, cols,
                    static_cast<float*>(X), (long long)ld);
   if (e != cudaSuccess) return DLLM_ERR_CUDA;
   count_launch();

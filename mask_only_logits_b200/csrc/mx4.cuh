@@ -23,6 +23,7 @@ namespace dllm {
 namespace mx4 {
 
 constexpr int kThreads = 256;
+constexpr int kGridPerSm = 64;          // quantize / dequantize: CTAs per SM, a warp per row
 
 __host__ __device__ inline long long scale_bytes(long long rows, int cols) {
   return (rows + 127) / 128 * ((cols + 127) / 128) * 512;
@@ -44,104 +45,118 @@ __device__ __forceinline__ uint32_t e2m1x2(float lo, float hi) {
   return r;
 }
 
-// One block: 32 values to 16 bytes of codes and the scale byte.
-__device__ __forceinline__ uint32_t quantize_block(const float (&x)[32], uint32_t (&q)[4]) {
-  uint32_t top = 0;                                    // |x| compares as its bit pattern
-#pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    const uint32_t b = __float_as_uint(x[i]) & 0x7fffffffu;
-    top = b > top ? b : top;
+// Eight neighbouring elements of a row, and what the quantisation asks of them: the bit pattern
+// of their largest size as fp32 (sizes compare as their bit patterns, two 16-bit ones at a time;
+// infinity and NaN come out as the largest), and their values.
+struct Eight16 {
+  uint4 v;
+  __device__ __forceinline__ void zero() { v = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ uint32_t top16() const {
+    const uint32_t m = 0x7fff7fffu;
+    const uint32_t t = __vmaxu2(__vmaxu2(v.x & m, v.y & m), __vmaxu2(v.z & m, v.w & m));
+    return max(t & 0xffffu, t >> 16);
   }
-  if (top >= 0x7f800000u) {                            // infinity or NaN
-#pragma unroll
-    for (int i = 0; i < 4; ++i) q[i] = 0;
-    return 0xffu;
+};
+template <typename T> struct Eight;
+template <> struct Eight<__nv_bfloat16> : Eight16 {
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = __ldg(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ uint32_t top() const { return top16() << 16; }
+  __device__ __forceinline__ float2 pair(int i) const {
+    const uint32_t w = i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
   }
-  int e = static_cast<int>(top >> 23) - 129;
-  e = e < -127 ? -127 : e;
-  const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    q[w] = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      q[w] |= e2m1x2(x[8 * w + 2 * i] * inv, x[8 * w + 2 * i + 1] * inv) << (8 * i);
+};
+template <> struct Eight<__half> : Eight16 {
+  __device__ __forceinline__ void load(const __half* p) { v = __ldg(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ uint32_t top() const {
+    return __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(top16())))) & 0x7fffffffu;
   }
-  return static_cast<uint32_t>(e + 127);
-}
+  __device__ __forceinline__ float2 pair(int i) const {
+    const uint32_t w = i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+  }
+};
+template <> struct Eight<float> {
+  float4 a, b;
+  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void load(const float* p) {
+    a = __ldg(reinterpret_cast<const float4*>(p));
+    b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  }
+  __device__ __forceinline__ uint32_t top() const {
+    const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    uint32_t t = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t = max(t, __float_as_uint(x[i]) & 0x7fffffffu);
+    return t;
+  }
+  __device__ __forceinline__ float2 pair(int i) const {
+    return i == 0 ? make_float2(a.x, a.y) : i == 1 ? make_float2(a.z, a.w)
+         : i == 2 ? make_float2(b.x, b.y) : make_float2(b.z, b.w);
+  }
+};
 
-__device__ __forceinline__ void load_block(const __nv_bfloat16* p, float (&x)[32]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      x[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
-      x[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-    }
-  }
-}
-__device__ __forceinline__ void load_block(const __half* p, float (&x)[32]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const __half2 h = *reinterpret_cast<const __half2*>(&w[j]);
-      x[8 * i + 2 * j] = __low2float(h);
-      x[8 * i + 2 * j + 1] = __high2float(h);
-    }
-  }
-}
-__device__ __forceinline__ void load_block(const float* p, float (&x)[32]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float4 v = __ldg(reinterpret_cast<const float4*>(p) + i);
-    x[4 * i] = v.x;
-    x[4 * i + 1] = v.y;
-    x[4 * i + 2] = v.z;
-    x[4 * i + 3] = v.w;
-  }
-}
+// A warp's piece of a row: kPiece elements in kSteps steps of 256, eight neighbouring elements
+// per lane (16 bytes of bf16, so that a warp's loads and stores are whole lines) and a block in
+// four lanes.  All loads are issued before the first is used.
+constexpr int kSteps = 4;
+constexpr int kPiece = 256 * kSteps;
 
-// Quantise block `blk` (of 4 * groups, those past K / 32 empty) of a row into codes row r and
-// scale row r; the four lanes of a 128-column group write their scale bytes as one word.
-// src: the row's first element, null for a row past the matrix (scales 0, no codes).
+// Quantise columns k0 .. k0 + kPiece - 1 of a row (src: its first element, null for a row past
+// the matrix: scales 0, no codes) into codes row r and scale row r.  Called by whole warps.
 template <typename T>
-__device__ __forceinline__ void quantize_to(const T* src, int blk, int K, int groups, long long r,
-                                            uint8_t* __restrict__ q, uint32_t* __restrict__ s) {
-  uint32_t scale = 0;
-  if (src != nullptr && blk * 32 < K) {
-    float x[32];
-    uint32_t c[4];
-    load_block(src + blk * 32, x);
-    scale = quantize_block(x, c);
-    *reinterpret_cast<uint4*>(q + r * (K / 2) + blk * 16) = make_uint4(c[0], c[1], c[2], c[3]);
+__device__ __forceinline__ void quantize_piece(const T* src, int k0, int K, int groups, long long r,
+                                               uint8_t* __restrict__ q, uint32_t* __restrict__ s) {
+  const int lane = threadIdx.x & 31;
+  Eight<T> x[kSteps];
+#pragma unroll
+  for (int j = 0; j < kSteps; ++j) {
+    const int k = k0 + 256 * j + 8 * lane;
+    if (src != nullptr && k < K) x[j].load(src + k);
+    else x[j].zero();
   }
-  const unsigned quad = 0xfu << (threadIdx.x & 28);    // the four lanes of this group
-  scale <<= 8 * (threadIdx.x & 3);
-  scale |= __shfl_xor_sync(quad, scale, 1);
-  scale |= __shfl_xor_sync(quad, scale, 2);
-  if ((threadIdx.x & 3) == 0) s[scale_word(r, blk >> 2, groups)] = scale;
+#pragma unroll
+  for (int j = 0; j < kSteps; ++j) {
+    if (k0 + 256 * j >= groups * 128) break;           // uniform: nothing of the row is left
+    const int k = k0 + 256 * j + 8 * lane;
+    uint32_t top = x[j].top();
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    const bool bad = top >= 0x7f800000u;               // infinity or NaN in the block
+    const int e = max(static_cast<int>(top >> 23) - 129, -127);
+    const float inv = bad ? 0.f : __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+    uint32_t codes = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 y = x[j].pair(i);
+      codes |= e2m1x2(y.x * inv, y.y * inv) << (8 * i);
+    }
+    const bool here = src != nullptr && k < K;
+    if (here) *reinterpret_cast<uint32_t*>(q + r * (K / 2) + k / 2) = bad ? 0u : codes;
+    // the scale bytes of four blocks (16 lanes) as one word
+    uint32_t w = here ? (bad ? 0xffu : static_cast<uint32_t>(e + 127)) << (8 * ((lane >> 2) & 3)) : 0u;
+    w |= __shfl_xor_sync(0xffffffffu, w, 4);
+    w |= __shfl_xor_sync(0xffffffffu, w, 8);
+    const int g = (k0 >> 7) + 2 * j + (lane >> 4);
+    if ((lane & 15) == 0 && g < groups) s[scale_word(r, g, groups)] = w;
+  }
 }
 
-// X [rows, K] (row stride ld elements) to MXFP4: one thread per block of 32.
+// X [rows, K] (row stride ld elements) to MXFP4: a warp per row, piece by piece.  Bound by HBM:
+// 2.53 bytes move per bf16 element (126464 x 4096: 218 us, 6.0 TB/s).  kGridPerSm CTAs per SM: a
+// grid of the 4 to 8 that are resident at once, each with many rows, took 12% longer.
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
 quantize_kernel(const T* __restrict__ X, long long rows, int K, long long ld, uint8_t* __restrict__ q,
                 uint32_t* __restrict__ s) {
   pdl_wait();
   pdl_launch_dependents();
-  const int groups = (K + 127) / 128, per_row = groups * 4;
-  const long long total = (rows + 127) / 128 * 128 * per_row;      // a multiple of 4
-  for (long long i = blockIdx.x * static_cast<long long>(kThreads) + threadIdx.x; i < total;
-       i += static_cast<long long>(gridDim.x) * kThreads) {
-    const long long r = i / per_row;
-    const int blk = static_cast<int>(i - r * per_row);
-    quantize_to(r < rows ? X + r * ld : static_cast<const T*>(nullptr), blk, K, groups, r, q, s);
-  }
+  const int groups = (K + 127) / 128;
+  const long long padded = (rows + 127) / 128 * 128;
+  const long long warps = static_cast<long long>(gridDim.x) * (kThreads / 32);
+  for (long long r = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); r < padded; r += warps)
+    for (int k0 = 0; k0 < groups * 128; k0 += kPiece)
+      quantize_piece(r < rows ? X + r * ld : static_cast<const T*>(nullptr), k0, K, groups, r, q, s);
 }
 
 // The masked rows H[row_idx[r]] (r < count) to MXFP4 rows r of q and s, and n_zero ints at
@@ -162,28 +177,30 @@ gather_quantize_kernel(const uint16_t* __restrict__ H, const int* __restrict__ r
     if (threadIdx.x == 0 && blockIdx.x == 0) atomicOr(status, kStatusCapacity);
     n = static_cast<int>(n_cap);
   }
-  const int groups = (d + 127) / 128, per_row = groups * 4;
-  const long long total = static_cast<long long>(n) * per_row;
-  for (long long i = blockIdx.x * static_cast<long long>(kThreads) + threadIdx.x; i < total;
-       i += static_cast<long long>(gridDim.x) * kThreads) {
-    const long long r = i / per_row;
-    const int blk = static_cast<int>(i - r * per_row);
+  // pieces of a row go to neighbouring warps, so that few rows still spread over the SMs
+  const int groups = (d + 127) / 128, pieces = (groups * 128 + kPiece - 1) / kPiece;
+  const long long items = static_cast<long long>(n) * pieces;
+  const long long warps = static_cast<long long>(gridDim.x) * (kThreads / 32);
+  for (long long i = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); i < items; i += warps) {
+    const int r = static_cast<int>(i / pieces), piece = static_cast<int>(i - static_cast<long long>(r) * pieces);
     const int p = row_idx[r];
     const bool bad = p < 0 || p >= n_pos;
-    if (bad && blk == 0) atomicOr(status, kStatusBounds);
-    quantize_to(bad ? static_cast<const __nv_bfloat16*>(nullptr)
-                    : reinterpret_cast<const __nv_bfloat16*>(H) + static_cast<size_t>(p) * d,
-                blk, d, groups, r, q, s);
+    if (bad && (threadIdx.x & 31) == 0) atomicOr(status, kStatusBounds);
+    quantize_piece(bad ? static_cast<const __nv_bfloat16*>(nullptr)
+                       : reinterpret_cast<const __nv_bfloat16*>(H) + static_cast<size_t>(p) * d,
+                   piece * kPiece, d, groups, r, q, s);
   }
 }
 
-// The value of an E2M1 code (4 bits).
-__device__ __forceinline__ float e2m1_value(uint32_t c) {
-  const uint32_t mag = c & 7u;
-  // 0 and .5, then 1 + mantissa / 2 scaled by 2^(exponent - 1)
-  const float v = mag < 2u ? 0.5f * static_cast<float>(mag)
-                           : __uint_as_float(((mag >> 1) + 126u) << 23 | (mag & 1u) << 22);
-  return (c & 8u) ? -v : v;
+// The values of two E2M1 codes (a byte, low nibble first).
+__device__ __forceinline__ float2 e2m1x2_values(uint32_t byte) {
+  uint32_t h;
+  asm("{\n\t.reg .b8 b, x;\n\t"
+      "cvt.u8.u32 b, %1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b;\n\t}"
+      : "=r"(h)
+      : "r"(byte));
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
 // 2^(s - 127), NaN for 0xFF (2^-127 is subnormal).
@@ -199,33 +216,50 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
     w[i] = *reinterpret_cast<const uint32_t*>(&h);
   }
-  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  __stcs(reinterpret_cast<uint4*>(p), make_uint4(w[0], w[1], w[2], w[3]));
 }
 __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+  __stcs(reinterpret_cast<float4*>(p), make_float4(v[0], v[1], v[2], v[3]));
+  __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(v[4], v[5], v[6], v[7]));
 }
 
-// The values an MXFP4 matrix stands for (bf16 or fp32: both exact): one thread per 8 elements.
+// The values an MXFP4 matrix stands for (bf16 or fp32: both exact): a warp per row, eight
+// elements per lane and step.
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
-dequantize_kernel(const uint8_t* __restrict__ q, const uint8_t* __restrict__ s, long long rows, int K,
+dequantize_kernel(const uint8_t* __restrict__ q, const uint32_t* __restrict__ s, long long rows, int K,
                   T* __restrict__ X, long long ld) {
   pdl_wait();
   pdl_launch_dependents();
-  const int groups = (K + 127) / 128, per_row = K / 8;
-  const long long total = rows * per_row;
-  for (long long i = blockIdx.x * static_cast<long long>(kThreads) + threadIdx.x; i < total;
-       i += static_cast<long long>(gridDim.x) * kThreads) {
-    const long long r = i / per_row;
-    const int c8 = static_cast<int>(i - r * per_row);
-    const uint32_t codes = __ldg(reinterpret_cast<const uint32_t*>(q) + i);
-    const int blk = c8 >> 2;
-    const float scale = e8m0_value(__ldg(s + 4 * scale_word(r, blk >> 2, groups) + (blk & 3)));
-    float v[8];
+  const int groups = (K + 127) / 128, lane = threadIdx.x & 31;
+  const long long warps = static_cast<long long>(gridDim.x) * (kThreads / 32);
+  for (long long r = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); r < rows; r += warps) {
+    for (int k0 = 8 * lane; k0 < K; k0 += kPiece) {
+      uint32_t codes[kSteps], words[kSteps];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = e2m1_value((codes >> (4 * j)) & 15u) * scale;
-    store8(X + r * ld + c8 * 8, v);
+      for (int j = 0; j < kSteps; ++j) {
+        const int k = k0 + 256 * j;
+        if (k < K) {
+          codes[j] = __ldcs(reinterpret_cast<const uint32_t*>(q + r * (K / 2) + k / 2));
+          words[j] = __ldg(s + scale_word(r, k >> 7, groups));
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kSteps; ++j) {
+        const int k = k0 + 256 * j;
+        if (k < K) {
+          const float scale = e8m0_value((words[j] >> (8 * ((k >> 5) & 3))) & 0xffu);
+          float v[8];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 y = e2m1x2_values((codes[j] >> (8 * i)) & 0xffu);
+            v[2 * i] = y.x * scale;
+            v[2 * i + 1] = y.y * scale;
+          }
+          store8(X + r * ld + k, v);
+        }
+      }
+    }
   }
 }
 

@@ -6,6 +6,10 @@
 //   z1 = c > 0 ? (z0 > 0 ? z0 / theta_b : z0 * theta_b) - presence_b - frequency_b * c : z0
 //   z2 = z1 + bias[b, v]
 //   z  = allowed(row, v) ? z2 : -inf
+// theta's reciprocal is rounded once per row: z * (1 / theta) is within one unit in the last
+// place of z / theta, and the 32 columns of a chunk stay free of the division's branches (with
+// them a chunk of penalised columns took 5000 cycles).
+//
 // The rules act on the accumulator chunk of 32 columns that the LM head's epilogue holds in
 // registers, so a shaped logit is never stored either; they are evaluated in fp32.
 //
@@ -20,6 +24,11 @@
 
 namespace dllm {
 namespace rules {
+
+// Two fp32 operations in one instruction (packed, each rounded as on its own).
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
 
 // The rules of one row: pointers into its sequence's and its bitmap's rows (null = no such rule).
 struct RowRules {
@@ -56,12 +65,12 @@ __device__ __forceinline__ RowRules row_rules(const dllm_logit_rules& r, int pos
   return o;
 }
 
-// theta's reciprocal is rounded once per row: z * inverse is within one unit in the last place
-// of z / theta, and the 32 columns of a chunk stay free of the division's branches (with them
-// a chunk of penalised columns took 5000 cycles).
-__device__ __forceinline__ float penalise(float z, int c, const RowRules& r) {
-  const float y = __fadd_rn(__fmul_rn(z, z > 0.f ? r.inverse : r.theta), -r.presence);
-  return fmaf(-r.frequency, static_cast<float>(c), y);
+// A read-only load that stays where it is written (the compiler would move one whose value is
+// needed much later down to its use).
+__device__ __forceinline__ uint32_t load_now(const void* p) {
+  uint32_t x;
+  asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(x) : "l"(p));
+  return x;
 }
 
 // The words of a row's two bitmaps that cover columns col0 .. col0+31 (col0 a multiple of 32;
@@ -72,43 +81,62 @@ struct Words {
 __device__ __forceinline__ Words load_words(int col0, int V, const RowRules& r) {
   const int left = V - col0;
   const uint32_t in = left >= 32 ? 0xffffffffu : (left > 0 ? (1u << left) - 1u : 0u);
-  return Words{r.seen && in ? __ldg(r.seen + (col0 >> 5)) & in : 0u,
-               r.allow && in ? __ldg(r.allow + (col0 >> 5)) & in : in};
+  Words w{0u, in};
+  if (r.seen && in) w.seen = load_now(r.seen + (col0 >> 5)) & in;
+  if (r.allow && in) w.ok = load_now(r.allow + (col0 >> 5)) & in;
+  return w;
 }
 
-__device__ __forceinline__ void prefetch_l1(const void* p) {
-  asm volatile("prefetch.global.L1 [%0];" ::"l"(p));
-}
-
-// Ask for the counts and biases that shape_chunk will read for this chunk.
-__device__ __forceinline__ void prefetch_chunk(int col0, int V, const RowRules& r, const Words& w) {
-  if (w.ok == 0u) return;
-  const int last = col0 + 31 < V ? col0 + 31 : V - 1;
-  if (w.seen != 0u) {
-    prefetch_l1(r.counts + col0);
-    prefetch_l1(r.counts + last);
-  }
-  if (r.bias != nullptr) {
-    prefetch_l1(r.bias + col0);
-    prefetch_l1(r.bias + last);
+__device__ __forceinline__ void ban(float (&v)[32], uint32_t ok) {
+  if (!__all_sync(0xffffffffu, ok == 0xffffffffu)) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (!((ok >> j) & 1u)) v[j] = -INFINITY;
   }
 }
 
 // Shape the 32 logits of columns col0 .. col0+31 of each lane's row; what is not allowed, and
-// columns at and past V, become -inf.  Called by all 32 lanes of a warp together: the tests
-// that skip a rule are taken for the warp, whose rows mostly share a sequence.  The biases are
-// asked for first, then `arrive` waits for the logits themselves.
-template <class Arrive>
-__device__ __forceinline__ void shape_chunk(float (&v)[32], int col0, int V, const RowRules& r,
-                                            const Words& w, Arrive&& arrive) {
-  const uint32_t any_seen = __reduce_or_sync(0xffffffffu, w.seen);
-  float4 bias[8];
-  const bool whole = r.bias != nullptr && col0 + 32 <= V;
-  if (whole) {
+// columns at and past V, become -inf.  Called by all 32 lanes of a warp together.
+//
+// shape_same: all rows of the warp have the same bias row and the same sequence's counts.  Then
+// column j's additive part (bias - presence - frequency * count, see additive) was fetched by
+// lane j ahead of time, one coalesced word per chunk, and stands in shared memory at `add`
+// (null: neither rule), from where every lane reads all 32.
+__device__ __forceinline__ void shape_same(float (&v)[32], const RowRules& r, const Words& w, const float* add) {
+  if (w.seen != 0u) {                          // the same word in every lane
 #pragma unroll
-    for (int j = 0; j < 8; ++j) bias[j] = __ldg(reinterpret_cast<const float4*>(r.bias + col0) + j);
+    for (int g = 0; g < 32; g += 8) {
+      if (((w.seen >> g) & 0xffu) == 0u) continue;
+#pragma unroll
+      for (int j = g; j < g + 8; ++j) {
+        const float y = v[j] * (v[j] > 0.f ? r.inverse : r.theta);
+        v[j] = (w.seen >> j) & 1u ? y : v[j];
+      }
+    }
   }
-  arrive();
+  if (add != nullptr) {
+#pragma unroll
+    for (int j = 0; j < 32; j += 4) {
+      const float4 b = *reinterpret_cast<const float4*>(add + j);
+      const float2 lo = add2(make_float2(v[j], v[j + 1]), make_float2(b.x, b.y));
+      const float2 hi = add2(make_float2(v[j + 2], v[j + 3]), make_float2(b.z, b.w));
+      v[j + 0] = lo.x;
+      v[j + 1] = lo.y;
+      v[j + 2] = hi.x;
+      v[j + 3] = hi.y;
+    }
+  }
+  ban(v, w.ok);
+}
+
+// The additive part of a column, of a bias and a count that were read for it.
+__device__ __forceinline__ float additive(float bias, int c, bool seen, const RowRules& r) {
+  return seen ? fmaf(-r.frequency, static_cast<float>(c), bias - r.presence) : bias;
+}
+
+// shape_mixed: the rows belong to several sequences; each lane reads its own.
+__device__ __forceinline__ void shape_mixed(float (&v)[32], int col0, int V, const RowRules& r, const Words& w) {
+  const uint32_t any_seen = __reduce_or_sync(0xffffffffu, w.seen);
   if (any_seen != 0u) {
     // eight columns at a time, without branches: all their counts are asked for before the
     // first is used
@@ -123,29 +151,29 @@ __device__ __forceinline__ void shape_chunk(float (&v)[32], int col0, int V, con
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float y = penalise(v[g + j], c[j], r);
-        v[g + j] = (w.seen >> (g + j)) & 1u ? y : v[g + j];
+        const float z = v[g + j];
+        const float y = z * (z > 0.f ? r.inverse : r.theta) + additive(0.f, c[j], true, r);
+        v[g + j] = (w.seen >> (g + j)) & 1u ? y : z;
       }
     }
   }
-  if (whole) {
+  if (r.bias != nullptr) {
+    if (col0 + 32 <= V) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      v[4 * j + 0] = __fadd_rn(v[4 * j + 0], bias[j].x);
-      v[4 * j + 1] = __fadd_rn(v[4 * j + 1], bias[j].y);
-      v[4 * j + 2] = __fadd_rn(v[4 * j + 2], bias[j].z);
-      v[4 * j + 3] = __fadd_rn(v[4 * j + 3], bias[j].w);
+      for (int j = 0; j < 32; j += 4) {
+        const float4 b = __ldg(reinterpret_cast<const float4*>(r.bias + col0 + j));
+        v[j + 0] += b.x;
+        v[j + 1] += b.y;
+        v[j + 2] += b.z;
+        v[j + 3] += b.w;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (col0 + j < V) v[j] += __ldg(r.bias + col0 + j);
     }
-  } else if (r.bias != nullptr) {
-#pragma unroll
-    for (int j = 0; j < 32; ++j)
-      if (col0 + j < V) v[j] = __fadd_rn(v[j], __ldg(r.bias + col0 + j));
   }
-  if (!__all_sync(0xffffffffu, w.ok == 0xffffffffu)) {
-#pragma unroll
-    for (int j = 0; j < 32; ++j)
-      if (!((w.ok >> j) & 1u)) v[j] = -INFINITY;
-  }
+  ban(v, w.ok);
 }
 
 // Running statistics of one row, as lm::RowState, with the rounding errors of s and t carried
@@ -189,20 +217,20 @@ __device__ __forceinline__ void fold(const float (&v)[32], int col0, State& st) 
   // of equal maxima the lower token wins; chunks come in any order
   const bool above = mx > st.m;
   if (above || (mx == st.m && col0 < st.a)) {
-    int j0 = 31;
+    uint32_t at = 0;                           // columns at the maximum
+    float c2 = -INFINITY;                      // the largest of the others
 #pragma unroll
-    for (int j = 31; j >= 0; --j)
-      if (v[j] == mx) j0 = j;
-    st.a = col0 + j0;
+    for (int j = 0; j < 32; ++j) {
+      if (v[j] == mx) at |= 1u << j;
+      else if constexpr (kExt) c2 = fmaxf(c2, v[j]);
+    }
+    st.a = col0 + __ffs(at) - 1;
     if (above) {
       const float f = ex2_approx((st.m - mx) * lm::kLog2e);
       if constexpr (kExt) {
-        float c2 = -INFINITY;                  // the chunk's second largest (mx again on a tie)
-#pragma unroll
-        for (int j = 0; j < 32; ++j) c2 = fmaxf(c2, j != j0 ? v[j] : -INFINITY);
         st.t = f > 0.f ? f * ((st.t - st.tc) + (st.m - mx) * (st.s - st.sc)) : 0.f;
         st.tc = 0.f;
-        st.m2 = fmaxf(st.m, c2);
+        st.m2 = (at & (at - 1u)) != 0u ? mx : fmaxf(st.m, c2);
       }
       st.s *= f;
       st.sc *= f;
@@ -212,25 +240,22 @@ __device__ __forceinline__ void fold(const float (&v)[32], int col0, State& st) 
   if constexpr (kExt) {
     if (!above) st.m2 = fmaxf(st.m2, mx);
   }
-  float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f, t0 = 0.f, t1 = 0.f;
+  const float2 shift = make_float2(-st.m, -st.m), log2e = make_float2(lm::kLog2e, lm::kLog2e);
+  float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+  float2 dev[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-  for (int j = 0; j < 32; j += 4) {
-    const float x0 = v[j] - st.m, x1 = v[j + 1] - st.m, x2 = v[j + 2] - st.m, x3 = v[j + 3] - st.m;
-    const float e0 = ex2_approx(x0 * lm::kLog2e), e1 = ex2_approx(x1 * lm::kLog2e);
-    const float e2 = ex2_approx(x2 * lm::kLog2e), e3 = ex2_approx(x3 * lm::kLog2e);
-    s0 += e0;
-    s1 += e1;
-    s2 += e2;
-    s3 += e3;
+  for (int j = 0; j < 16; ++j) {
+    float2 x = add2(make_float2(v[2 * j], v[2 * j + 1]), shift);
+    const float2 y = mul2(x, log2e);
+    const float2 e = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+    sum[j & 1] = add2(sum[j & 1], e);
     if constexpr (kExt) {                      // e is 0 long before x reaches the bound
-      t0 = fmaf(e0, fmaxf(x0, -1e4f), t0);
-      t1 = fmaf(e1, fmaxf(x1, -1e4f), t1);
-      t0 = fmaf(e2, fmaxf(x2, -1e4f), t0);
-      t1 = fmaf(e3, fmaxf(x3, -1e4f), t1);
+      x = make_float2(fmaxf(x.x, -1e4f), fmaxf(x.y, -1e4f));
+      dev[j & 1] = fma2(e, x, dev[j & 1]);
     }
   }
-  kahan(st.s, st.sc, (s0 + s1) + (s2 + s3));
-  if constexpr (kExt) kahan(st.t, st.tc, t0 + t1);
+  kahan(st.s, st.sc, (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y));
+  if constexpr (kExt) kahan(st.t, st.tc, (dev[0].x + dev[0].y) + (dev[1].x + dev[1].y));
 }
 
 // Merge another part of the vocabulary's statistics into st; of equal maxima the lower token

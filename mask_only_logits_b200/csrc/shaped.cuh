@@ -25,12 +25,18 @@
 //             tiles and about 0.62 of them: frequent tokens sit at the low ids of a vocabulary,
 //             so a stream of consecutive tiles would get all the penalised columns (99 us where
 //             the others took 65, 256 rows of d2048 V151936).
+//   sums      The tensor cores drop what does not fit fp32 at every addition (K = 16), always
+//             towards zero: over d = 4096 a large bf16 logit came out 5e-6 too small.  An
+//             accumulator therefore holds a piece of K; the epilogue adds the pieces up in
+//             registers (128 a thread, dealt to the epilogue's warpgroups by setmaxnreg), which
+//             leaves 0.6e-6 to 1.4e-6, about an fp32 sum's error.  MXFP4 products are a few bits wide and their sums exact.
 //   epilogue  eight warps: two per TMEM lane quadrant, each with half of a tile's columns (the
 //             rules and scores cost more instructions than the plain statistics, and four MXFP4
-//             tiles take the time of one bf16 tile).  rules::shape_chunk on each 32 logits, then
+//             tiles take the time of one bf16 tile).  rules on each 32 logits, then
 //             the fold and merge of rules.cuh.  Warps without a masked row only release the
-//             accumulator.  The bitmap words of a tile are loaded, and its counts and biases
-//             asked for, before the wait for its accumulator.
+//             accumulator.  Rows of one warp mostly share a sequence: what its rules read for a
+//             tile then comes as one coalesced word per chunk and array, fetched during the
+//             tile before; loaded where it is used it held each chunk up by 2 us.
 //   merge     of at most 32 rows: a warp per row, its lanes over the splits (a row's partials
 //             then come in one or two rounds of loads instead of one per eight splits).
 #pragma once
@@ -69,14 +75,15 @@ constexpr int kEpiFirst = 4;
 constexpr int kThreads = 32 * (kEpiFirst + kEpiWarps);
 
 // Shared memory: barriers and flags, two blocks of row states (the halves of a tile meet there),
-// then the ring.
+// per epilogue warp the additive rules of its half of a tile, then the ring.
 constexpr int kMaxStages = 8;
 constexpr int kHeadBytes = 512;
 constexpr int kCombBytes = 2 * 128 * 20;
-constexpr int kRingOffset = 6144;
 constexpr int kSmemBytes = 232448;                   // all of a CTA's 227 KB
-constexpr int kRingBytes = kSmemBytes - 1024 - kRingOffset;
-static_assert(kHeadBytes + kCombBytes <= kRingOffset && kRingOffset % 1024 == 0, "shared-memory layout");
+template <class Op>
+constexpr int ring_offset() {
+  return (kHeadBytes + kCombBytes + kEpiWarps * (Op::BN / 2) * 4 + 1023) / 1024 * 1024;
+}
 
 template <int CG, class Op>
 struct Cfg {
@@ -156,6 +163,17 @@ __device__ __forceinline__ uint64_t scale_desc(uint32_t smem_addr) {
          (static_cast<uint64_t>(1u) << 46);
 }
 
+// Registers of a thread, moved between the warpgroups of a CTA: 384 threads start with 168 each,
+// 3 x 168 = 72 + 2 x 216.
+template <int N>
+__device__ __forceinline__ void give_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void take_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // True in one lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
@@ -174,6 +192,7 @@ struct Smem {
   volatile int* last_flag;
   struct RowStateRaw { float m, s, t, m2; int a; };
   RowStateRaw* comb;
+  float* add;
   uint8_t* ring;
   int stages;
   uint32_t b_off, stage_bytes;
@@ -191,10 +210,11 @@ struct Smem {
     abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
     last_flag = abort_flag + 1;
     comb = reinterpret_cast<RowStateRaw*>(base + kHeadBytes);
-    ring = base + kRingOffset;
+    add = reinterpret_cast<float*>(base + kHeadBytes + kCombBytes);
+    ring = base + ring_offset<Op>();
     b_off = boxes * C::A_BOX;
     stage_bytes = b_off + C::B_BYTES + Op::SFA + Op::SFB;
-    stages = kRingBytes / stage_bytes;
+    stages = (kSmemBytes - 1024 - ring_offset<Op>()) / stage_bytes;
     if (stages > kMaxStages) stages = kMaxStages;
   }
   __device__ __forceinline__ uint32_t a(int s) const { return smem_u32(ring) + s * stage_bytes; }
@@ -299,6 +319,18 @@ __device__ __forceinline__ void run(uint8_t* smem_raw, const Maps& tm, int count
   const Plan pl = Plan::make(count, plan_v<Op>(p.V), static_cast<int>(gridDim.x) / CG, C::kGroupM, C::BM);
   const int holder = static_cast<int>(blockIdx.x) / CG;
   const int KB = (p.d + Op::BK - 1) / Op::BK;
+  // Stages summed in one accumulator (bf16; MXFP4 a tile's whole K).  Single CTAs: 512 of K; W's
+  // way from HBM hides the epilogue's extra reads (one row d4096 V126464: 179 us, unsplit 173).
+  // Pairs: a quarter of K, at least 512: with it the error stays by that of an fp32 sum, which
+  // grows with K too.  256 rows d2048 V151936 with all rules: 512 219 us, 768 209, 1024 188,
+  // unsplit 173; 1024 rows d4096 V126464: 907, 876, 832, 800 us (both under the power cap).
+  int piece_stages = KB;
+  if (!Op::kMx4) {
+    const int quarter = (KB + 3) / 4;
+    const int most = CG == 1 || quarter < 8 ? 8 : quarter;
+    const int pieces = (KB + most - 1) / most;
+    piece_stages = (KB + pieces - 1) / pieces;
+  }
   // the schedule's vocabulary tile i, in the order of the walk
   auto tile_at = [&](int i) {
     const unsigned n = static_cast<unsigned>(pl.numN), u = static_cast<unsigned>(i), v = static_cast<unsigned>(p.tile_step);
@@ -314,8 +346,9 @@ __device__ __forceinline__ void run(uint8_t* smem_raw, const Maps& tm, int count
     return got;
   };
 
-  if (warp == 0) {
-    if (lane == 0) {
+  if (warp < kEpiFirst) {
+    if constexpr (!Op::kMx4) give_registers<72>();
+    if (warp == 0 && lane == 0) {
       // ------------------------------ TMA producer ------------------------------
       Turn at;
 #ifdef DLLM_FAULT_SKIP_STAGE
@@ -403,21 +436,22 @@ __device__ __forceinline__ void run(uint8_t* smem_raw, const Maps& tm, int count
         return true;
       };
       lm::for_each_tile(pl, holder, load_tile);
-    }
-  } else if (warp == 1) {
-    if (leader) {
+    } else if (warp == 1 && leader) {
       // ------------------------------ MMA issuer --------------------------------
       Turn at, sat, old;          // places in the ring and the scales' ring; the stage whose scale
       int ahead = 0;              // columns come next
-      uint32_t tile = 0;
+      uint32_t piece = 0;
       auto mma_tile = [&](int, int i) -> bool {
         const int n = tile_at(i);
-        const uint32_t buf = tile & 1u, tph = (tile >> 1) & 1u;
-        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.tempty[buf]), tph ^ 1u, abort_flag, status)))
-          return false;
-        tc_fence_after();
-        const uint32_t d_tmem = tmem_base + buf * BN;
-        for (int kb = 0; kb < KB; ++kb) {
+        for (int kb = 0, kp = 0; kb < KB; ++kb) {                // kp: stage within its accumulator
+          const uint32_t buf = piece & 1u;
+          const uint32_t d_tmem = tmem_base + buf * BN;
+          if (kp == 0) {
+            const uint32_t ph = (piece >> 1) & 1u;
+            if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.tempty[buf]), ph ^ 1u, abort_flag, status)))
+              return false;
+            tc_fence_after();
+          }
           bool got = mbar_wait(smem_u32(&sm.full[at.s]), at.ph, abort_flag, status);
           if constexpr (Op::kMx4) {
             if (ahead < Op::kSfRing) {
@@ -436,7 +470,7 @@ __device__ __forceinline__ void run(uint8_t* smem_raw, const Maps& tm, int count
             if (elect_one()) {
 #pragma unroll
               for (int k = 0; k < Op::BK / Op::UK; ++k)
-                lm::mma_issue<CG>(d_tmem, adesc + 2 * k, bdesc + 2 * k, C::kIdesc, (kb | k) != 0 ? 1u : 0u);
+                lm::mma_issue<CG>(d_tmem, adesc + 2 * k, bdesc + 2 * k, C::kIdesc, (kp | k) != 0 ? 1u : 0u);
               lm::mma_commit_all<CG>(empty);            // stage free once these MMAs retire
             }
           } else {
@@ -477,10 +511,13 @@ __device__ __forceinline__ void run(uint8_t* smem_raw, const Maps& tm, int count
           }
           __syncwarp();
           at.next(sm.stages);
+          if (++kp == piece_stages || kb == KB - 1) {
+            if (elect_one()) lm::mma_commit_all<CG>(smem_u32(&sm.tfull[buf]));   // accumulator ready
+            __syncwarp();
+            ++piece;
+            kp = 0;
+          }
         }
-        if (elect_one()) lm::mma_commit_all<CG>(smem_u32(&sm.tfull[buf]));   // accumulator ready
-        __syncwarp();
-        ++tile;
         return true;
       };
       if (!wait_tmem() || !lm::for_each_tile(pl, holder, mma_tile)) {
@@ -491,7 +528,8 @@ __device__ __forceinline__ void run(uint8_t* smem_raw, const Maps& tm, int count
         __syncwarp();
       }
     }
-  } else if (warp >= kEpiFirst) {
+  } else {
+    if constexpr (!Op::kMx4) take_registers<216>();
     // -------------------------------- epilogue ---------------------------------
     const int q = warp & 3;                      // TMEM lane quadrant of this warp
     const int half = (warp - kEpiFirst) >> 2;            // which half of a tile's columns
@@ -500,14 +538,60 @@ __device__ __forceinline__ void run(uint8_t* smem_raw, const Maps& tm, int count
     const int row_in_tile = static_cast<int>(rank) * C::BM_CTA + row_in_cta;
     bool ok = wait_tmem();
     const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + half * (BN / 2);
-    uint32_t tile = 0, epi_phase = 0, units_done = 0;
+    uint32_t piece = 0, epi_phase = 0, units_done = 0;
     bool live = false;                // live: this warp holds a masked row of the m-tile
     rules::RowRules rr = rules::no_rules();
+    // rules: whether all of the warp's rows share them (rules::shape_same), and the additive part
+    // of this warp's columns of the current tile
+    bool same = false;
+    float* const add = sm.add + (warp - kEpiFirst) * (BN / 2);
+    const bool has_add = kRules && (rule_set.bias != nullptr || rule_set.counts != nullptr);
     auto enter_m_tile = [&](int m_tile) {
-      live = m_tile * C::BM + row_in_tile - lane < count;
+      const int row = m_tile * C::BM + row_in_tile;
+      live = row - lane < count;
       if constexpr (kRules) {
-        const int row = m_tile * C::BM + row_in_tile;
-        rr = row < count ? rules::row_rules(rule_set, p.row_idx[row], p.L, status) : rules::no_rules();
+        if (live) {                              // lanes past the last row take its rules
+          rr = rules::row_rules(rule_set, p.row_idx[row < count ? row : count - 1], p.L, status);
+          const float* b0 = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(rr.bias), 0));
+          const int* c0 = reinterpret_cast<const int*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(rr.counts), 0));
+          same = __all_sync(0xffffffffu, rr.bias == b0 && rr.counts == c0);
+        }
+      }
+    };
+    // What the rules of a tile read, fetched while the tile before it is worked on: the bitmap
+    // words, and (rows alike) lane j's bias and count of column j of each chunk.
+    struct Fetched {
+      rules::Words w[kChunks];
+      float bias[kChunks];
+      int c[kChunks];
+    };
+    auto fetch = [&](int n, Fetched& f) {
+      if constexpr (kRules) {
+        const int first = n * BN + half * (BN / 2);
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+          const int col = first + 32 * c + lane;
+          f.w[c] = rules::load_words(first + 32 * c, p.V, rr);
+          f.bias[c] = 0.f;
+          f.c[c] = 0;
+          if (same && col < p.V) {
+            if (rr.bias) f.bias[c] = __uint_as_float(rules::load_now(rr.bias + col));
+            if (rr.counts) f.c[c] = static_cast<int>(rules::load_now(rr.counts + col));
+          }
+        }
+      }
+    };
+    // ... becomes the current tile's: words in registers, the additive parts in shared memory
+    rules::Words words[kChunks] = {};
+    auto settle = [&](const Fetched& f) {
+      if constexpr (kRules) {
+        __syncwarp();                            // no lane still reads the tile before
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+          words[c] = f.w[c];
+          if (same && has_add)
+            add[32 * c + lane] = rules::additive(f.bias[c], f.c[c], (f.w[c].seen >> lane) & 1u, rr);
+        }
         __syncwarp();
       }
     };
@@ -519,57 +603,100 @@ __device__ __forceinline__ void run(uint8_t* smem_raw, const Maps& tm, int count
       epi_phase ^= 1u;
       return __all_sync(0xffffffffu, got);
     };
-    // fold this warp's half of the next accumulator (vocabulary tile n) into st
-    auto consume = [&](int n, rules::State& st) -> bool {
-      const uint32_t buf = tile & 1u, tph = (tile >> 1) & 1u;
-      const int first = n * BN + half * (BN / 2);
-      rules::Words w[kChunks];
-      if constexpr (kRules) {
-        if (live) {
-#pragma unroll
-          for (int c = 0; c < kChunks; ++c) w[c] = rules::load_words(first + 32 * c, p.V, rr);
-#pragma unroll
-          for (int c = 0; c < kChunks; ++c) rules::prefetch_chunk(first + 32 * c, p.V, rr, w[c]);
-        }
-      }
-      const bool got = mbar_wait(smem_u32(&sm.tfull[buf]), tph, abort_flag, status);
+    // the next accumulator; false (warp-uniform) if the CTA is aborting
+    auto wait_piece = [&]() -> bool {
+      const bool got = mbar_wait(smem_u32(&sm.tfull[piece & 1u]), (piece >> 1) & 1u, abort_flag, status);
       if (!__all_sync(0xffffffffu, got)) return false;
       tc_fence_after();
-      if (live) {
-        const uint32_t taddr = lane_base + buf * BN;
-#pragma unroll 1
-        for (int c = 0; c < kChunks; ++c) {
-          float v[32];
-          const int col0 = first + c * 32;
-          tmem_ld32(taddr + c * 32, v);
-          if constexpr (kRules) {
-            const rules::Words wc = w[0];
-#pragma unroll
-            for (int k = 1; k < kChunks; ++k) w[k - 1] = w[k];       // the next chunk's words
-            if (__reduce_or_sync(0xffffffffu, wc.ok) == 0u) {
-              tmem_ld_wait();
-              continue;
-            }
-            rules::shape_chunk(v, col0, p.V, rr, wc, [] { tmem_ld_wait(); });
-          } else {
-            tmem_ld_wait();
-            if (col0 + 32 > p.V) {
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (col0 + j >= p.V) v[j] = -INFINITY;
-            }
-          }
-          rules::fold<kExt>(v, col0, st);
-        }
-      }
+      return true;
+    };
+    // release it: the leader's MMA waits for the epilogues of both CTAs
+    auto release_piece = [&]() {
       tc_fence_before();
       __syncwarp();
-      // release the accumulator: the leader's MMA waits for the epilogues of both CTAs
-      if (lane == 0) {
-        if constexpr (CG == 2) mbar_arrive_cluster(smem_u32(&sm.tempty[buf]), 0u);
+      const uint32_t bar = smem_u32(&sm.tempty[piece & 1u]);
+      if constexpr (CG == 2) {
+        if (lane == 0) mbar_arrive_cluster(bar, 0u);
+      } else {
+        if (lane < 2) mbar_arrive(bar);          // twice: the barrier counts both CTAs of a pair
       }
-      if (CG == 1 && lane < 2) mbar_arrive(smem_u32(&sm.tempty[buf]));    // twice: it counts both variants
-      ++tile;
+      ++piece;
+    };
+    // shape 32 logits (chunk c of the tile, columns col0 ..) and fold them into st
+    auto take = [&](float (&v)[32], int c, int col0, const rules::Words& w, rules::State& st) {
+      if constexpr (kRules) {
+        if (__reduce_or_sync(0xffffffffu, w.ok) == 0u) return;
+        if (same) rules::shape_same(v, rr, w, has_add ? add + 32 * c : nullptr);
+        else rules::shape_mixed(v, col0, p.V, rr, w);
+      } else if (col0 + 32 > p.V) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (col0 + j >= p.V) v[j] = -INFINITY;
+      }
+      rules::fold<kExt>(v, col0, st);
+    };
+    // fold this warp's half of vocabulary tile n into st; the unit's next tile is `next` (-1: none)
+    auto consume = [&](int n, int next, rules::State& st) -> bool {
+      const int first = n * BN + half * (BN / 2);
+      Fetched f;
+      if constexpr (Op::kMx4) {
+        if (!wait_piece()) return false;
+        if (live) {
+          if (next >= 0) fetch(next, f);
+          const uint32_t taddr = lane_base + (piece & 1u) * BN;
+#pragma unroll 1
+          for (int c = 0; c < kChunks; ++c) {
+            float v[32];
+            tmem_ld32(taddr + c * 32, v);
+            const rules::Words w = words[0];
+#pragma unroll
+            for (int k = 1; k < kChunks; ++k) words[k - 1] = words[k];   // the next chunk's
+            tmem_ld_wait();
+            take(v, c, first + 32 * c, w, st);
+          }
+        }
+        release_piece();
+      } else {
+        float acc[kChunks][32];
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+          for (int j = 0; j < 32; ++j) acc[c][j] = 0.f;
+#pragma unroll 1
+        for (int kb = 0; kb < KB; kb += piece_stages) {
+          if (!wait_piece()) return false;
+          if (live) {
+            const uint32_t taddr = lane_base + (piece & 1u) * BN;
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) {
+              float v[32];
+              tmem_ld32(taddr + c * 32, v);
+              tmem_ld_wait();
+#pragma unroll
+              for (int j = 0; j < 32; j += 2) {
+                const float2 y = rules::add2(make_float2(acc[c][j], acc[c][j + 1]), make_float2(v[j], v[j + 1]));
+                acc[c][j] = y.x;
+                acc[c][j + 1] = y.y;
+              }
+            }
+          }
+          release_piece();
+        }
+        if (live) {
+          if (next >= 0) fetch(next, f);
+#pragma unroll 1
+          for (int c = 0; c < kChunks; ++c) {
+            take(acc[0], c, first + 32 * c, words[0], st);
+#pragma unroll
+            for (int k = 1; k < kChunks; ++k) {                          // the next chunk's
+              words[k - 1] = words[k];
+#pragma unroll
+              for (int j = 0; j < 32; ++j) acc[k - 1][j] = acc[k][j];
+            }
+          }
+        }
+      }
+      if (live && next >= 0) settle(f);
       return true;
     };
     auto write_result = [&](int row, const RowState& st) {
@@ -592,7 +719,7 @@ __device__ __forceinline__ void run(uint8_t* smem_raw, const Maps& tm, int count
       c.m2 = st.m2;
       c.a = st.a;
     };
-    auto add = [&](int block, int r, RowState& st) {
+    auto join = [&](int block, int r, RowState& st) {
       const auto& c = sm.comb[block * C::BM_CTA + r];
       rules::merge<kExt>(st, c.m, c.s, c.a, c.t, c.m2);
     };
@@ -611,7 +738,7 @@ __device__ __forceinline__ void run(uint8_t* smem_raw, const Maps& tm, int count
       const int block = units_done++ & 1;
       if (half == 1) put(block, row_in_cta, st);
       if (!epi_sync()) return false;
-      if (half == 0) add(block, row_in_cta, st);
+      if (half == 0) join(block, row_in_cta, st);
       if (units == 1) {
         if (half == 0 && valid) write_result(row, st);
         return true;
@@ -655,16 +782,16 @@ __device__ __forceinline__ void run(uint8_t* smem_raw, const Maps& tm, int count
         }
       } else {
         // each warp takes half of the slots, of its own quadrant's rows; the halves meet as above
-        const int mid = units / 2, join = units_done++ & 1;
+        const int mid = units / 2, next_block = units_done++ & 1;
         RowState acc;
         acc.reset();
         if (valid)
           acc = merge_slots<kExt>(p.part, p.part_a, base0 + row_in_cta, stride, half ? mid : 0,
                                   half ? units : mid, 1, u.P, j_lo);
-        if (half == 1) put(join, row_in_cta, acc);
+        if (half == 1) put(next_block, row_in_cta, acc);
         if (!epi_sync()) return false;
         if (half == 0 && valid) {
-          add(join, row_in_cta, acc);
+          join(next_block, row_in_cta, acc);
           write_result(row, acc);
         }
       }
@@ -681,18 +808,26 @@ __device__ __forceinline__ void run(uint8_t* smem_raw, const Maps& tm, int count
       int m_local = u.leftover ? static_cast<int>(u.i0 / pl.rr) : u.m_local;
       bool fresh = true;
       for (int j = 0; j < n_tiles && ok; ++j) {
-        int i = u.n0 + j, next_m = m_local;
+        int i = u.n0 + j, i_next = i + 1, next_m = m_local;
         if (u.leftover) {
           i = u.P * pl.rb + static_cast<int>((u.i0 + j) % pl.rr);
+          i_next = u.P * pl.rb + static_cast<int>((u.i0 + j + 1) % pl.rr);
           next_m = static_cast<int>((u.i0 + j + 1) / pl.rr);
         }
+        const int n = tile_at(i);
+        const bool last = j + 1 == n_tiles || next_m != m_local;
         if (fresh) {
           st.reset();
           enter_m_tile(g * pl.gmax + m_local);
+          if (live) {
+            Fetched f;
+            fetch(n, f);
+            settle(f);
+          }
           fresh = false;
         }
-        ok = consume(tile_at(i), st);
-        if (ok && (j + 1 == n_tiles || next_m != m_local)) {
+        ok = consume(n, last ? -1 : tile_at(i_next), st);
+        if (ok && last) {
           ok = finish(g, u, m_local, u.p, st);
           m_local = next_m;
           fresh = true;

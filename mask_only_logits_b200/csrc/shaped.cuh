@@ -19,8 +19,10 @@
 //             operands pass through vector registers and a stage took 0.53 us to issue.
 //   ring      as many stages as fit: what bounds the staging is the bytes in flight (a stage
 //             comes 2 us after it is asked for when every SM loads).
-//   A rows    single CTAs load their rows of Hm in boxes of 32, only as many as are masked,
-//             and give the rest of the tile's room to more stages.
+//   A rows    single CTAs load their rows of Hm in boxes of 32, only as many as are masked; the
+//             rest of the operand's 128 rows is zeroed once: the tensor cores' power depends on
+//             what they multiply, and streaming W for one row runs at the power cap (one row
+//             d4096 V126464, back to back: bf16 195.3 -> 191.8 us, MXFP4 65.4 -> 64.4 us).
 //   order     the schedule's vocabulary tile i is tile i * step mod (tiles), step coprime to the
 //             tiles and about 0.62 of them: frequent tokens sit at the low ids of a vocabulary,
 //             so a stream of consecutive tiles would get all the penalised columns (99 us where
@@ -181,7 +183,7 @@ __device__ __forceinline__ bool elect_one() {
   return r != 0;
 }
 
-// Addresses in shared memory.  A stage: [Hm rows, boxes x 4 KB | W rows | scales of Hm | of W].
+// Addresses in shared memory.  A stage: [Hm rows | W rows | scales of Hm | scales of W].
 template <int CG, class Op>
 struct Smem {
   using C = Cfg<CG, Op>;
@@ -194,10 +196,11 @@ struct Smem {
   RowStateRaw* comb;
   float* add;
   uint8_t* ring;
-  int stages;
-  uint32_t b_off, stage_bytes;
+  static constexpr uint32_t kA = 4 * C::A_BOX, kStageBytes = kA + C::B_BYTES + Op::SFA + Op::SFB;
+  static constexpr int kFit = (kSmemBytes - 1024 - ring_offset<Op>()) / static_cast<int>(kStageBytes);
+  static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
 
-  __device__ __forceinline__ Smem(uint8_t* raw, int boxes) {
+  __device__ __forceinline__ explicit Smem(uint8_t* raw) {
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     full = reinterpret_cast<uint64_t*>(base);
     empty = full + kMaxStages;
@@ -212,13 +215,9 @@ struct Smem {
     comb = reinterpret_cast<RowStateRaw*>(base + kHeadBytes);
     add = reinterpret_cast<float*>(base + kHeadBytes + kCombBytes);
     ring = base + ring_offset<Op>();
-    b_off = boxes * C::A_BOX;
-    stage_bytes = b_off + C::B_BYTES + Op::SFA + Op::SFB;
-    stages = (kSmemBytes - 1024 - ring_offset<Op>()) / stage_bytes;
-    if (stages > kMaxStages) stages = kMaxStages;
   }
-  __device__ __forceinline__ uint32_t a(int s) const { return smem_u32(ring) + s * stage_bytes; }
-  __device__ __forceinline__ uint32_t b(int s) const { return a(s) + b_off; }
+  __device__ __forceinline__ uint32_t a(int s) const { return smem_u32(ring) + s * kStageBytes; }
+  __device__ __forceinline__ uint32_t b(int s) const { return a(s) + kA; }
   __device__ __forceinline__ uint32_t sfa(int s) const { return b(s) + C::B_BYTES; }
   __device__ __forceinline__ uint32_t sfb(int s) const { return sfa(s) + Op::SFA; }
 };
@@ -291,9 +290,8 @@ __device__ __forceinline__ void run(uint8_t* smem_raw, const Maps& tm, int count
   constexpr int BN = Op::BN;
   count_raw = __shfl_sync(0xffffffffu, count_raw, 0);              // warp-uniform, and known to be
   const int count = count_raw < 0 ? 0 : (count_raw > p.n_cap ? p.n_cap : count_raw);
-  // boxes of 32 rows that hold a CTA's rows (one m-tile of fewer than 128 rows needs fewer)
-  const int a_boxes = CG == 2 || count >= C::BM_CTA ? 4 : (count > 0 ? (count + 31) / 32 : 1);
-  const Smem<CG, Op> sm(smem_raw, a_boxes);
+  const Smem<CG, Op> sm(smem_raw);
+  constexpr int kStages = Smem<CG, Op>::kStages;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // uniform
   const uint32_t rank = CG == 1 ? 0u : cluster_ctarank();
   const bool leader = rank == 0;
@@ -399,7 +397,7 @@ __device__ __forceinline__ void run(uint8_t* smem_raw, const Maps& tm, int count
         const int b_row = n * BN + static_cast<int>(rank) * C::B_ROWS;
         const int valid = count - a_row;
         const int boxes = valid >= C::BM_CTA ? 4 : (valid + 31) / 32;          // CG = 1: valid >= 1
-        for (int kb = 0; kb < KB; ++kb, at.next(sm.stages)) {
+        for (int kb = 0; kb < KB; ++kb, at.next(kStages)) {
           const int s = at.s;
           const uint32_t ph = at.ph;
           if (!mbar_wait(smem_u32(&sm.empty[s]), ph ^ 1u, abort_flag, status)) return false;
@@ -458,7 +456,7 @@ __device__ __forceinline__ void run(uint8_t* smem_raw, const Maps& tm, int count
               ++ahead;
             } else {              // the MMAs that read these scale columns are done
               got = got && mbar_wait(smem_u32(&sm.empty[old.s]), old.ph, abort_flag, status);
-              old.next(sm.stages);
+              old.next(kStages);
             }
           }
           if (!__all_sync(0xffffffffu, got)) return false;
@@ -510,7 +508,7 @@ __device__ __forceinline__ void run(uint8_t* smem_raw, const Maps& tm, int count
             sat.next(Op::kSfRing);
           }
           __syncwarp();
-          at.next(sm.stages);
+          at.next(kStages);
           if (++kp == piece_stages || kb == KB - 1) {
             if (elect_one()) lm::mma_commit_all<CG>(smem_u32(&sm.tfull[buf]));   // accumulator ready
             __syncwarp();
@@ -847,7 +845,7 @@ __device__ __forceinline__ void run(uint8_t* smem_raw, const Maps& tm, int count
   if (aborted) {                // loads already issued land before shared memory is released
     if (warp == 0 && lane == 0 && leader) {
       const unsigned long long deadline = globaltimer_ns() + kWaitLimitNs;
-      for (int s = 0; s < sm.stages; ++s)
+      for (int s = 0; s < kStages; ++s)
         if (armed_mask & (1u << s))
           if (!mbar_wait_until(smem_u32(&sm.full[s]), (armed_parity >> s) & 1u, deadline, status)) break;
     }
@@ -874,7 +872,7 @@ shaped_kernel(const __grid_constant__ CUtensorMap tmA1, const __grid_constant__ 
               const __grid_constant__ dllm_logit_rules rule_set) {
   extern __shared__ uint8_t smem_raw[];
   // What no variant changes is set up while the staging kernel still runs.
-  const Smem<1, Op> sm(smem_raw, 1);
+  const Smem<1, Op> sm(smem_raw);
   if (threadIdx.x == 0) {
     for (int s = 0; s < kMaxStages; ++s) {
       mbar_init(smem_u32(&sm.full[s]), 1);
@@ -899,6 +897,11 @@ shaped_kernel(const __grid_constant__ CUtensorMap tmA1, const __grid_constant__ 
       tma_prefetch_desc(&tmSB);
     }
   }
+  // rows of Hm that single CTAs do not load count as zero; the loads (asynchronous proxy) come after
+  for (int s = 0; s < sm.kStages; ++s)
+    for (uint32_t i = threadIdx.x; i < sm.kA / 16; i += kThreads)
+      reinterpret_cast<uint4*>(sm.ring + s * sm.kStageBytes)[i] = make_uint4(0u, 0u, 0u, 0u);
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   cluster_sync();               // barriers of both CTAs initialised before any remote use
   pdl_wait();
   pdl_launch_dependents();

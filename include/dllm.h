@@ -515,8 +515,8 @@ typedef struct dllm_logit_rules {
  * arguments, outputs and errors as in dllm_masked_logits_window; further errors:
  * DLLM_ERR_NULL (counts without seen or seen without counts, a penalty without counts,
  * allow_id without allow), DLLM_ERR_ALIGN (a pointer that is not 16-byte aligned),
- * DLLM_ERR_SHAPE (a stride too small, bias_stride not a multiple of 4, allow_rows < 1 or, without allow_id,
- * neither 1 nor B).
+ * DLLM_ERR_SHAPE (V > 2^30, a stride too small, bias_stride not a multiple of 4, allow_rows < 1
+ * or, without allow_id, neither 1 nor B).
  */
 dllm_status dllm_masked_logits_rules(const uint16_t* H, const uint8_t* M, const uint16_t* W,
                                      int32_t B, int32_t L, int32_t d, int32_t V,
@@ -538,7 +538,7 @@ dllm_status dllm_masked_logits_rules(const uint16_t* H, const uint8_t* M, const 
  *            n_valid = n_sel of a selection, those a step has just unmasked.
  *   counts   device int32 [B, V].      seen  device uint32 [B, ceil(V / 32)].
  * tokens may be NULL if n == 0.  Errors: DLLM_ERR_NULL, DLLM_ERR_ALIGN, DLLM_ERR_SHAPE (B < 1,
- * B > 65535, n < 0, V < 1, accumulate not 0/1), DLLM_ERR_CUDA, DLLM_ERR_DEVICE.
+ * B > 65535, n < 0, V < 1 or > 2^30, accumulate not 0/1), DLLM_ERR_CUDA, DLLM_ERR_DEVICE.
  */
 dllm_status dllm_token_counts(const int32_t* tokens, const uint8_t* M, const int32_t* n_valid,
                               int32_t B, int32_t n, int32_t V, int32_t accumulate,
@@ -560,7 +560,7 @@ dllm_status dllm_token_counts(const int32_t* tokens, const uint8_t* M, const int
  *            0xFF = NaN) in tiles of 128 rows by 4 blocks; the byte of row r, block j = k / 32
  *            is at ((r / 128) * ceil(cols / 128) + j / 4) * 512 + (r % 32) * 16
  *            + ((r / 32) % 4) * 4 + j % 4; the rest of the tiles holds 0.
- * Constraints: rows >= 1, cols a positive multiple of 32.  Errors: DLLM_ERR_NULL,
+ * Constraints: 1 <= rows < 2^31, cols a positive multiple of 32, at most 2^30.  Errors: DLLM_ERR_NULL,
  * DLLM_ERR_ALIGN, DLLM_ERR_SHAPE, DLLM_ERR_CUDA, DLLM_ERR_DEVICE.
  */
 #define DLLM_BF16 0

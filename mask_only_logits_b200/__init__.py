@@ -544,10 +544,10 @@ def token_counts(tokens, counts, seen, M=None, n_valid=None, accumulate=False, s
     unmasked.  Ids outside [0, V) are skipped."""
     B, n = tokens.shape
     V = counts.shape[-1]
-    if tuple(counts.shape) != (B, V) or tuple(seen.shape) != (B, _bitmap_words(V)):
+    if counts.shape != (B, V) or seen.shape != (B, (V + 31) // 32):
         raise ValueError(f"counts, seen: expected [{B}, V] and [{B}, ceil(V / 32)], got "
                          f"{list(counts.shape)} and {list(seen.shape)}")
-    if seen.dtype not in (torch.int32, torch.uint32):
+    if seen.dtype is not torch.int32 and seen.dtype is not torch.uint32:
         raise ValueError(f"seen: expected torch.int32, got {seen.dtype}")
     dev = _call_device(counts)
     _check(lib().dllm_token_counts(
@@ -599,8 +599,11 @@ def _mx4_args(X, q, s, dtypes, stream) -> tuple:
     rows, cols = X.shape
     if cols % 32 != 0 or cols == 0:
         raise ValueError(f"X: {cols} columns are not a positive multiple of 32")
-    ptr, ld = _rows_ptr(X, dtypes, "X", rows, cols)
     dev = _call_device(X)
+    if dev >= 0 and X.dtype in dtypes and X.is_contiguous():
+        ptr, ld = X.data_ptr(), cols
+    else:
+        ptr, ld = _rows_ptr(X, dtypes, "X", rows, cols)
     return (ptr, _MX4_DTYPES[X.dtype], rows, cols, ld,
             _arg(q, torch.uint8, "q", rows * (cols // 2), dev),
             _arg(s, torch.uint8, "s", -(-rows // 128) * -(-cols // 128) * 512, dev),

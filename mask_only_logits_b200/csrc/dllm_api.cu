@@ -86,6 +86,27 @@ inline void count_launch(int n = 1) {
   if (g_prof.on) g_prof.kernel_launches += n;
 }
 
+// The event pair around a GEMM launch: records the first and hands out the second.
+bool prof_gemm_start(cudaStream_t s, cudaEvent_t* stop) {
+  if (!g_prof.on) return true;
+  if (g_prof.used + 2 > g_prof.ev.size()) {
+    for (int i = 0; i < 64; ++i) {
+      cudaEvent_t e;
+      if (cudaEventCreate(&e) != cudaSuccess) return false;
+      g_prof.ev.push_back(e);
+    }
+  }
+  cudaEventRecord(g_prof.ev[g_prof.used], s);
+  *stop = g_prof.ev[g_prof.used + 1];
+  g_prof.used += 2;
+  return true;
+}
+void prof_gemm_stop(cudaStream_t s, cudaEvent_t stop) {
+  if (!g_prof.on) return;
+  cudaEventRecord(stop, s);
+  g_prof.gemm_launches++;
+}
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Launch with programmatic stream serialization: the kernel may start while the previous
@@ -148,6 +169,15 @@ dllm_status device_state(DeviceState** out) {
            cudaFuncSetAttribute(shaped::shaped_kernel<shaped::Mx4, false, true>, smem_attr, shaped::kSmemBytes) ||
            cudaFuncSetAttribute(rules::token_count_kernel, smem_attr, rules::kCountMaxSlice * 4)))
         st.err = DLLM_ERR_CUDA;
+      // the bf16 kernels of shaped.cuh deal their registers out anew: what the warpgroups take must be
+      // what the launch gave them, or they would wait for the rest
+      cudaFuncAttributes fa0, fa1;
+      if (st.err == DLLM_OK &&
+          (cudaFuncGetAttributes(&fa0, shaped::shaped_kernel<shaped::Bf16, true, false>) ||
+           cudaFuncGetAttributes(&fa1, shaped::shaped_kernel<shaped::Bf16, true, true>)))
+        st.err = DLLM_ERR_CUDA;
+      if (st.err == DLLM_OK && (fa0.numRegs != shaped::kLaunchRegs || fa1.numRegs != shaped::kLaunchRegs))
+        st.err = DLLM_ERR_DEVICE;
       if (st.err == DLLM_OK) {
         // how many CTA pairs of the paired GEMM can be resident at once (a persistent grid
         // larger than that would serialise)
@@ -448,20 +478,8 @@ dllm_status run_logits(const LogitsArgs& a, bool debug, bool skip_prepare = fals
   if (cg != 1 && make_tmap(&tmB2, a.W, static_cast<uint64_t>(a.V), a.d, lm::BN / 2) != DLLM_OK)
     return DLLM_ERR_CUDA;
 
-  cudaEvent_t e0 = nullptr, e1 = nullptr;
-  if (g_prof.on) {
-    if (g_prof.used + 2 > g_prof.ev.size()) {
-      for (int i = 0; i < 64; ++i) {
-        cudaEvent_t e;
-        if (cudaEventCreate(&e) != cudaSuccess) return DLLM_ERR_CUDA;
-        g_prof.ev.push_back(e);
-      }
-    }
-    e0 = g_prof.ev[g_prof.used];
-    e1 = g_prof.ev[g_prof.used + 1];
-    g_prof.used += 2;
-    cudaEventRecord(e0, a.s);
-  }
+  cudaEvent_t e1 = nullptr;
+  if (!prof_gemm_start(a.s, &e1)) return DLLM_ERR_CUDA;
   {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
@@ -511,18 +529,16 @@ dllm_status run_logits(const LogitsArgs& a, bool debug, bool skip_prepare = fals
     if (e != cudaSuccess) return DLLM_ERR_CUDA;
   }
   count_launch();
-  if (g_prof.on) {
-    cudaEventRecord(e1, a.s);
-    g_prof.gemm_launches++;
-  }
+  prof_gemm_stop(a.s, e1);
   return cudaPeekAtLastError() == cudaSuccess ? DLLM_OK : DLLM_ERR_CUDA;
 }
 
 // ---------------------------------------------------------------------------------------
 // Rules on the logits, and MXFP4 operands (dllm_masked_logits_rules, dllm_masked_logits_mx4)
 // ---------------------------------------------------------------------------------------
+constexpr int kMaxColumns = 1 << 30;             // vocabulary tiles and columns stay in 32 bits
 bool logits_shape_ok(int B, int L, int d, int V) {
-  return shapes_ok(B, L) && V >= 1 && d >= DLLM_D_MULTIPLE && d % DLLM_D_MULTIPLE == 0;
+  return shapes_ok(B, L) && V >= 1 && V <= kMaxColumns && d >= DLLM_D_MULTIPLE && d % DLLM_D_MULTIPLE == 0;
 }
 
 dllm_status validate_rules(const dllm_logit_rules& r, int B, int V) {
@@ -617,6 +633,8 @@ dllm_status launch_shaped(const ShapedArgs& x, const DeviceState& ds, const WsLa
   const dllm_logit_rules rules = x.rules ? *x.rules : dllm_logit_rules{};
   const int* count = a.count;
   const int variant = g_gemm_variant.load();
+  cudaEvent_t stop = nullptr;
+  if (!prof_gemm_start(a.s, &stop)) return DLLM_ERR_CUDA;
 #define DLLM_LAUNCH_SHAPED(RULES, EXT)                                                            \
   cudaLaunchKernelEx(&cfg, shaped::shaped_kernel<Op, RULES, EXT>, tmA1, tmA2, tmB1, tmB2, tmSA,    \
                      tmSB, count, variant, p, rules)
@@ -632,6 +650,7 @@ dllm_status launch_shaped(const ShapedArgs& x, const DeviceState& ds, const WsLa
 #undef DLLM_LAUNCH_SHAPED
   if (e != cudaSuccess) return DLLM_ERR_CUDA;
   count_launch();
+  prof_gemm_stop(a.s, stop);
   return cudaPeekAtLastError() == cudaSuccess ? DLLM_OK : DLLM_ERR_CUDA;
 }
 
@@ -687,7 +706,8 @@ dllm_status run_shaped(const ShapedArgs& x) {
 dllm_status mx4_checks(const void* X, int dtype, bool f16_ok, int64_t rows, int32_t cols, int64_t ld,
                        const void* q, const void* s) {
   if (!X || !q || !s) return DLLM_ERR_NULL;
-  if (rows < 1 || rows >= (1ll << 31) || cols < 32 || cols % 32 != 0 || ld < cols) return DLLM_ERR_SHAPE;
+  if (rows < 1 || rows >= (1ll << 31) || cols < 32 || cols % 32 != 0 || cols > kMaxColumns || ld < cols)
+    return DLLM_ERR_SHAPE;
   if (dtype != DLLM_BF16 && dtype != DLLM_F32 && !(f16_ok && dtype == DLLM_F16)) return DLLM_ERR_SHAPE;
   if (!aligned16(X) || !aligned16(q) || !aligned16(s) || ld % (dtype == DLLM_F32 ? 4 : 8) != 0)
     return DLLM_ERR_ALIGN;
@@ -1131,7 +1151,7 @@ dllm_status dllm_token_counts(const int32_t* tokens, const uint8_t* M, const int
                               void* stream) {
   const dllm::NvtxRange nvtx_range("dllm_token_counts");
   if ((!tokens && n != 0) || !counts || !seen) return DLLM_ERR_NULL;
-  if (B < 1 || B > 65535 || n < 0 || V < 1 || (accumulate != 0 && accumulate != 1)) return DLLM_ERR_SHAPE;
+  if (B < 1 || B > 65535 || n < 0 || V < 1 || V > kMaxColumns || (accumulate != 0 && accumulate != 1)) return DLLM_ERR_SHAPE;
   const void* ptrs[] = {tokens, M, n_valid, counts, seen};
   for (const void* p : ptrs)
     if (p && !aligned16(p)) return DLLM_ERR_ALIGN;
@@ -1159,7 +1179,7 @@ dllm_status dllm_token_counts(const int32_t* tokens, const uint8_t* M, const int
 }
 
 size_t dllm_mx4_scale_bytes(int64_t rows, int32_t cols) {
-  if (rows < 1 || rows >= (1ll << 31) || cols < 32 || cols % 32 != 0) return 0;
+  if (rows < 1 || rows >= (1ll << 31) || cols < 32 || cols % 32 != 0 || cols > kMaxColumns) return 0;
   return static_cast<size_t>(mx4::scale_bytes(rows, cols));
 }
 

@@ -199,6 +199,13 @@ struct State {
   }
 };
 
+// The largest of three, NaN if one of them is.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 __device__ __forceinline__ void kahan(float& sum, float& over, float x) {
   const float y = x - over;
   const float n = sum + y;
@@ -212,8 +219,14 @@ template <bool kExt>
 __device__ __forceinline__ void fold(const float (&v)[32], int col0, State& st) {
   float mx = v[0];
 #pragma unroll
-  for (int j = 1; j < 32; ++j) mx = fmaxf(mx, v[j]);
+  for (int j = 1; j < 31; j += 2) mx = max3(mx, v[j], v[j + 1]);
+  mx = max3(mx, v[31], v[31]);
   if (mx == -INFINITY) return;                 // nothing allowed in this chunk
+  if (mx != mx) {                              // a NaN: so are the row's statistics
+    st.s = mx;
+    if constexpr (kExt) st.t = mx;
+    return;
+  }
   // of equal maxima the lower token wins; chunks come in any order
   const bool above = mx > st.m;
   if (above || (mx == st.m && col0 < st.a)) {
@@ -262,7 +275,7 @@ __device__ __forceinline__ void fold(const float (&v)[32], int col0, State& st) 
 // wins, so the parts may come in any order.
 template <bool kExt>
 __device__ __forceinline__ void merge(lm::RowState& st, float m, float s, int a, float t, float m2) {
-  if (m == -INFINITY) return;
+  if (m == -INFINITY && s == 0.f) return;      // nothing allowed (a sum that is NaN goes on)
   if (m > st.m) {
     const float f = ex2_approx((st.m - m) * lm::kLog2e);
     if constexpr (kExt) {
@@ -284,10 +297,11 @@ __device__ __forceinline__ void merge(lm::RowState& st, float m, float s, int a,
 }
 
 // Final values of a row.  Nothing allowed: no token, no confidence, and the worst of each
-// score, so that a selection takes such a row last.
+// score, so that a selection takes such a row last.  A row whose every logit is NaN has NaN
+// statistics and token 0.
 __device__ __forceinline__ void finish(const lm::RowState& st, int& tok, float& conf, float& lse,
                                        float& ent, float& margin) {
-  if (st.m == -INFINITY) {
+  if (st.m == -INFINITY && st.s == 0.f) {
     tok = -1;
     conf = 0.f;
     lse = -INFINITY;

@@ -165,8 +165,10 @@ __device__ __forceinline__ uint64_t scale_desc(uint32_t smem_addr) {
          (static_cast<uint64_t>(1u) << 46);
 }
 
-// Registers of a thread, moved between the warpgroups of a CTA: 384 threads start with 168 each,
-// 3 x 168 = 72 + 2 x 216.
+// Registers of a thread, moved between the warpgroups of a CTA (bf16): 384 threads start with
+// kLaunchRegs each (the host checks that the build has them).
+constexpr int kLaunchRegs = 168, kProducerRegs = 72, kEpilogueRegs = 216;
+static_assert(kProducerRegs + 2 * kEpilogueRegs <= 3 * kLaunchRegs, "more registers than the launch has");
 template <int N>
 __device__ __forceinline__ void give_registers() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
@@ -345,7 +347,7 @@ __device__ __forceinline__ void run(uint8_t* smem_raw, const Maps& tm, int count
   };
 
   if (warp < kEpiFirst) {
-    if constexpr (!Op::kMx4) give_registers<72>();
+    if constexpr (!Op::kMx4) give_registers<kProducerRegs>();
     if (warp == 0 && lane == 0) {
       // ------------------------------ TMA producer ------------------------------
       Turn at;
@@ -527,7 +529,7 @@ __device__ __forceinline__ void run(uint8_t* smem_raw, const Maps& tm, int count
       }
     }
   } else {
-    if constexpr (!Op::kMx4) take_registers<216>();
+    if constexpr (!Op::kMx4) take_registers<kEpilogueRegs>();
     // -------------------------------- epilogue ---------------------------------
     const int q = warp & 3;                      // TMEM lane quadrant of this warp
     const int half = (warp - kEpiFirst) >> 2;            // which half of a tile's columns

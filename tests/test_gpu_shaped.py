@@ -413,6 +413,36 @@ def test_first_of_equal_maxima(dl, mx4, variant):
     assert (o["margin"] == 0).all()
 
 
+@pytest.mark.parametrize("mx4", [False, True], ids=["bf16", "mx4"])
+def test_nan_and_infinity_stay_where_they_are(dl, mx4):
+    """A hidden row with a NaN has NaN statistics (not those of a row that may take nothing), the
+    rows beside it theirs; a NaN bias on a banned token is never seen; unmasked rows are not read."""
+    B, L, d, V = 1, 40, 128, 700
+    H, M, W = head_inputs(B, L, d, V, "half", seed=6)
+    pos = np.flatnonzero(M.numpy().reshape(-1))
+    clean = H.clone()
+    H[np.setdiff1d(np.arange(L), pos)] = float("nan")
+    H[pos[3], 5] = float("nan")
+    H[pos[4], 7] = float("inf")
+    bits = np.ones((1, V), dtype=bool)
+    bits[0, ::7] = False
+    bias = np.zeros(V, dtype=np.float32)
+    bias[::7] = np.nan
+    r = reference(clean, M, W, mx4, dict(allow=S.pack_bits(bits)))
+    rules = dl.LogitRules(B, L, V, bias=torch.from_numpy(bias).cuda(),
+                          allow=torch.from_numpy(S.pack_bits(bits)).cuda())
+    o = outputs(L, B, ALL)
+    ws = torch.full((max(dl.workspace_bytes(B, L, d, V), dl.workspace_bytes_mx4(B, L, d, V)),), 0xFF,
+                    dtype=torch.uint8, device="cuda")
+    call(dl, mx4, H.cuda(), M.cuda(), dl.Mx4Matrix.quantize(W.cuda()) if mx4 else W.cuda(), rules, ALL, o, ws)
+    assert dl.get_status() == 0
+    for k in ("conf", "lse", "entropy"):
+        assert torch.isnan(o[k][3:5]).all(), k
+    keep = np.delete(np.arange(len(pos)), [3, 4])
+    check({k: (v if v is None else v[:len(pos)][torch.from_numpy(keep).cuda()]) for k, v in o.items()
+           if k in ("tok", "conf", "lse", "entropy", "margin")}, {k: v[keep] for k, v in r.items()}, V, ALL)
+
+
 def test_bitmap_number_out_of_range_is_recorded(dl):
     """A bitmap number past the table is reported and its row left unrestricted; the others keep
     their bitmaps."""
@@ -547,3 +577,38 @@ def test_c_struct_layout(dl):
     """The binding's struct is the header's: eight pointers, four 64-bit strides, one int."""
     from mask_only_logits_b200 import _abi
     assert ctypes.sizeof(_abi.LogitRulesStruct) == 13 * 8
+
+
+@pytest.mark.parametrize("mx4", [False, True], ids=["bf16", "mx4"])
+@pytest.mark.parametrize("variant", [1, 2], ids=["single", "pair"])
+def test_unarmed_stage_times_out(dl, mx4, variant):
+    """A copy of the library that leaves one stage of the ring unarmed: the waits give up after a
+    second, every role unwinds, the host reads DLLM_ERR_TIMEOUT, and the regular library computes
+    right afterwards.  Nothing faults or hangs."""
+    import os
+
+    from mask_only_logits_b200 import _abi, build
+    out = os.path.join(build.PKG_DIR, "libdllm_fault_skip_stage.so")
+    if not os.path.exists(out) or os.path.getmtime(out) < os.path.getmtime(build.LIB_PATH):
+        build.build(extra_flags=["-DDLLM_FAULT_SKIP_STAGE=1"], out=out)
+    lib = _abi.load_from(out)
+    B, L, d, V = 1, 300, 512, 2000
+    H, M, W = head_inputs(B, L, d, V, "all", seed=1)
+    ref_rules, dev = make_rules(["penalty"], B, L, V, seed=1)
+    rules = dl.LogitRules(B, L, V, **dev)
+    Wd = dl.Mx4Matrix.quantize(W.cuda()) if mx4 else W.cuda()
+    Hd, Md, o = H.cuda(), M.cuda(), outputs(L, B, 0)
+    ws = torch.empty(max(dl.workspace_bytes(B, L, d, V), dl.workspace_bytes_mx4(B, L, d, V)),
+                     dtype=torch.uint8, device="cuda")
+    p = lambda t: ctypes.c_void_p(t.data_ptr())                        # noqa: E731
+    nul, stream = ctypes.c_void_p(None), ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    head = [p(Hd), p(Md)] + ([p(Wd.q), p(Wd.s)] if mx4 else [p(Wd)]) + [B, L, d, V, nul, nul]
+    tail = [0, p(o["tok"]), p(o["conf"]), p(o["lse"]), nul, nul, p(o["row_idx"]), p(o["seq_off"]),
+            p(o["count"]), p(ws), ws.numel(), stream]
+    fn = lib.dllm_masked_logits_mx4 if mx4 else lib.dllm_masked_logits_rules
+    assert lib.dllm_debug_set_gemm_variant(variant) == 0
+    assert fn(*head, ctypes.byref(rules._struct), *tail) == 0
+    assert lib.dllm_get_status(stream) == -6 and lib.dllm_get_status(stream) == 0
+    call(dl, mx4, Hd, Md, Wd, rules, 0, o, ws)
+    assert dl.get_status() == 0
+    check(o, reference(H, M, W, mx4, ref_rules), V, 0)

@@ -24,6 +24,7 @@
 #include "mx4.cuh"
 #include "rules.cuh"
 #include "shaped.cuh"
+#include "stage.cuh"
 
 #ifndef DLLM_GATHER_HOST_CTAS
 #define DLLM_GATHER_HOST_CTAS 1   // gather CTAs per SM when the rows come from host memory
@@ -654,25 +655,38 @@ dllm_status launch_shaped(const ShapedArgs& x, const DeviceState& ds, const WsLa
   return cudaPeekAtLastError() == cudaSuccess ? DLLM_OK : DLLM_ERR_CUDA;
 }
 
-// Compaction, and the masked rows of H in MXFP4 into the workspace (prepare_rows for bf16).
-dllm_status prepare_rows_mx4(const LogitsArgs& a, const DeviceState& ds, const WsLayout& w) {
+// Compaction, and the masked rows of H into the workspace: in MXFP4, or as they are.
+dllm_status stage_shaped(const LogitsArgs& a, const DeviceState& ds, const WsLayout& w, bool mx4) {
   const void* Hd = nullptr;
   const void* Md = nullptr;
-  bool host_rows = false;
-  dllm_status st = resolve_input(a.H, &Hd, &host_rows);
+  bool h_host = false, m_host = false;
+  dllm_status st = resolve_input(a.H, &Hd, &h_host);
   if (st != DLLM_OK) return st;
-  if ((st = resolve_input(a.M, &Md)) != DLLM_OK) return st;
+  if ((st = resolve_input(a.M, &Md, &m_host)) != DLLM_OK) return st;
   uint8_t* ws = static_cast<uint8_t*>(a.ws);
-  if ((st = launch_compact(static_cast<const uint8_t*>(Md), a.B, a.L, a.win_lo, a.win_hi, a.row_idx,
-                           a.seq_off, a.count, reinterpret_cast<int*>(ws + w.tiles_off), ds.status,
-                           a.s)) != DLLM_OK)
-    return st;
-  if (launch_pdl(mx4::gather_quantize_kernel, dim3(ds.sms * (host_rows ? DLLM_GATHER_HOST_CTAS : 4)),
-                 dim3(mx4::kThreads), 0, a.s, static_cast<const uint16_t*>(Hd), (const int*)a.row_idx,
-                 (const int*)a.count, static_cast<long long>(a.B) * a.L, w.rows, a.d, ws + w.hm_off,
-                 reinterpret_cast<uint32_t*>(ws + w.hs_off), reinterpret_cast<int*>(ws + w.ctr_off),
-                 w.n_ctr, ds.status) != cudaSuccess)
-    return DLLM_ERR_CUDA;
+  const uint8_t* M = static_cast<const uint8_t*>(Md);
+  const uint16_t* H = static_cast<const uint16_t*>(Hd);
+  uint8_t* rows = ws + w.hm_off;
+  uint32_t* scales = reinterpret_cast<uint32_t*>(ws + w.hs_off);
+  int* ctr = reinterpret_cast<int*>(ws + w.ctr_off);
+  const long long n = static_cast<long long>(a.B) * a.L;
+  cudaError_t e;
+  if (n <= stage::kMaxPositions && !m_host) {          // a mask in host memory is read once, not by every CTA
+    const dim3 grid(stage::kCtas), thr(stage::kThreads);
+    e = mx4 ? launch_pdl(stage::stage_rows_kernel<true>, grid, thr, 0, a.s, M, a.B, a.L, a.win_lo, a.win_hi, H,
+                         a.d, w.rows, a.row_idx, a.seq_off, a.count, rows, scales, ctr, w.n_ctr, ds.status)
+            : launch_pdl(stage::stage_rows_kernel<false>, grid, thr, 0, a.s, M, a.B, a.L, a.win_lo, a.win_hi, H,
+                         a.d, w.rows, a.row_idx, a.seq_off, a.count, rows, scales, ctr, w.n_ctr, ds.status);
+  } else {
+    if (!mx4) return prepare_rows(a, ds, w);
+    if ((st = launch_compact(M, a.B, a.L, a.win_lo, a.win_hi, a.row_idx, a.seq_off, a.count,
+                             reinterpret_cast<int*>(ws + w.tiles_off), ds.status, a.s)) != DLLM_OK)
+      return st;
+    e = launch_pdl(mx4::gather_quantize_kernel, dim3(ds.sms * (h_host ? DLLM_GATHER_HOST_CTAS : 4)),
+                   dim3(mx4::kThreads), 0, a.s, H, (const int*)a.row_idx, (const int*)a.count, n, w.rows, a.d,
+                   rows, scales, ctr, w.n_ctr, ds.status);
+  }
+  if (e != cudaSuccess) return DLLM_ERR_CUDA;
   count_launch();
   return DLLM_OK;
 }
@@ -697,8 +711,7 @@ dllm_status run_shaped(const ShapedArgs& x) {
   if (w.rows < 1) return DLLM_ERR_WORKSPACE;
   DeviceState* ds = nullptr;
   if ((st = device_state(&ds)) != DLLM_OK) return st;
-  st = mx4 ? prepare_rows_mx4(a, *ds, w) : prepare_rows(a, *ds, w);
-  if (st != DLLM_OK) return st;
+  if ((st = stage_shaped(a, *ds, w, mx4)) != DLLM_OK) return st;
   const lm::Outputs outs{a.tok, a.conf, a.lse, a.entropy, a.margin, a.raw, 0};
   return mx4 ? launch_shaped<shaped::Mx4>(x, *ds, w, outs) : launch_shaped<shaped::Bf16>(x, *ds, w, outs);
 }

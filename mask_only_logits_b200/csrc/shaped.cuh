@@ -224,6 +224,11 @@ struct Smem {
   __device__ __forceinline__ uint32_t sfb(int s) const { return sfa(s) + Op::SFA; }
 };
 
+// The MMA warp waits for the release of the stage whose scale columns it is about to rewrite; with
+// fewer stages than that the barrier could be a whole turn ahead.
+static_assert(Smem<1, Mx4>::kStages >= Mx4::kSfRing && Smem<2, Mx4>::kStages >= Mx4::kSfRing,
+              "the ring is shorter than the scales' ring");
+
 // Position in the ring: stage, and the parity of its current use.
 struct Turn {
   int s = 0;

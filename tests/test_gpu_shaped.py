@@ -299,18 +299,19 @@ def test_mx4_without_rules(dl, shape, ext):
 
 @pytest.mark.parametrize("mx4", [False, True], ids=["bf16", "mx4"])
 def test_mask_of_many_positions(dl, mx4):
-    """More positions than one launch stages (65536), and exactly as many: the same rows."""
+    """As many positions as one launch stages (2048), one more, and several tiles of the mask; every
+    position of the smallest masked, and a sequence of one position each."""
     d, V = 64, 300
-    for B, L in ((2, 32768), (3, 21846)):
+    for B, L, k in ((2, 1024, 2048), (2048, 1, 700), (1, 2049, 2049), (3, 683, 1500), (2, 32768, 200)):
         H, M, W = head_inputs(B, L, d, V, "none", seed=9)
-        pos = np.sort(np.random.default_rng(1).choice(B * L, 200, replace=False))
+        pos = np.sort(np.random.default_rng(1).choice(B * L, k, replace=False))
         M.view(-1)[pos] = 1
         M[B - 1, L - 1] = 1
         pos = np.flatnonzero(M.numpy().reshape(-1))
         ref_rules, dev = make_rules(["penalty", "grammar"], B, L, V, seed=1)
         r = reference(H, M, W, mx4, ref_rules, pos)
         o = outputs(B * L, B, ALL)
-        ws = torch.empty((dl.workspace_bytes_mx4 if mx4 else dl.workspace_bytes_rows)(B, L, d, V, 300),
+        ws = torch.empty((dl.workspace_bytes_mx4 if mx4 else dl.workspace_bytes_rows)(B, L, d, V, k + 1),
                          dtype=torch.uint8, device="cuda")
         call(dl, mx4, H.cuda(), M.cuda(), dl.Mx4Matrix.quantize(W.cuda()) if mx4 else W.cuda(),
              dl.LogitRules(B, L, V, **dev), ALL, o, ws)

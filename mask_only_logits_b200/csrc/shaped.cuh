@@ -260,32 +260,66 @@ struct Problem {
   int* status;
 };
 
+// Add one to a counter with release and acquire order.
+__device__ __forceinline__ int count_unit(int* ctr) {
+  int old;
+  asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(old) : "l"(ctr) : "memory");
+  return old;
+}
+
 // The partials of one row in slots i0, i0 + step, .. below i1 (streams 0 .. P - 1, then remainder
-// holders from j_lo), merged.  All loads of a round are issued before any is used; kept out of
-// line so that its registers do not weigh on the epilogue's loop.
+// holders from j_lo), merged four at a time: the next four are on their way meanwhile, and the
+// four's sums are taken against their maximum, so that no partial waits for another.  A short
+// loop, out of line: it runs once at the end of a launch, from a cold instruction cache (unrolled
+// to 8 or 18 partials the merge of 72 x 128 took 12 and 10 us).
 template <bool kExt>
 __device__ __noinline__ RowState merge_slots(const float4* part, const int* part_a, long long base,
                                              long long stride, int i0, int i1, int step, int P, int j_lo) {
-  constexpr int kRound = 8;
+  constexpr int kRound = 4;
   RowState acc;
   acc.reset();
+  float4 v[kRound], next[kRound];                // m, s, t, m2
+  int a[kRound], next_a[kRound];
+#pragma unroll
+  for (int k = 0; k < kRound; ++k) {
+    v[k] = make_float4(-INFINITY, 0.f, 0.f, -INFINITY);
+    a[k] = 0;
+  }
 #pragma unroll 1
-  for (; i0 < i1; i0 += kRound * step) {
-    float4 v[kRound];
-    int a[kRound];
+  for (int i = i0; i < i1 + kRound * step; i += kRound * step) {     // the last turn merges the rest
 #pragma unroll
     for (int k = 0; k < kRound; ++k) {
-      const int i = i0 + k * step;
-      const long long e = base + (i < P ? i : i + j_lo) * stride;
-      v[k] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
-      a[k] = 0;
-      if (i < i1) {
-        v[k] = __ldcg(part + e);
-        a[k] = __ldcg(part_a + e);
+      const int slot = i + k * step;
+      const long long e = base + (slot < P ? slot : slot + j_lo) * stride;
+      next[k] = make_float4(-INFINITY, 0.f, 0.f, -INFINITY);
+      next_a[k] = 0;
+      if (slot < i1) {
+        next[k] = __ldcg(part + e);
+        next_a[k] = __ldcg(part_a + e);
       }
     }
+    float m = acc.m;
 #pragma unroll
-    for (int k = 0; k < kRound; ++k) rules::merge<kExt>(acc, v[k].x, v[k].y, a[k], v[k].z, v[k].w);
+    for (int k = 0; k < kRound; ++k) {
+      if constexpr (kExt) acc.m2 = fmaxf(fmaxf(acc.m2, v[k].w), fminf(m, v[k].x));
+      m = fmaxf(m, v[k].x);
+    }
+    // nothing allowed anywhere yet: the sums are 0 (or NaN, which stays)
+    const float shift = m == -INFINITY ? 0.f : m;
+    const float f = ex2_approx((acc.m - shift) * lm::kLog2e);
+    if constexpr (kExt) acc.t = f > 0.f ? f * (acc.t + (acc.m - shift) * acc.s) : 0.f;
+    acc.s *= f;
+    if (acc.m != m) acc.a = 0x7fffffff;
+    acc.m = m;
+#pragma unroll
+    for (int k = 0; k < kRound; ++k) {
+      const float d = v[k].x - shift, g = ex2_approx(d * lm::kLog2e);
+      acc.s += v[k].x == -INFINITY ? v[k].y : v[k].y * g;
+      if constexpr (kExt) acc.t += g > 0.f ? g * (v[k].z + d * v[k].y) : 0.f;
+      if (v[k].x == m) acc.a = min(acc.a, a[k]);   // of equal maxima the lower token
+      v[k] = next[k];
+      a[k] = next_a[k];
+    }
   }
   return acc;
 }
@@ -757,13 +791,11 @@ __device__ __forceinline__ void run(uint8_t* smem_raw, const Maps& tm, int count
           atomicOr(status, kStatusBounds);             // cannot happen: workspace sized for it
         }
       }
-      // Once all partials are written, one thread fences (for the whole CTA: its fence follows the
-      // meeting), counts the unit and fences again; the last unit's CTA reads through L2.
+      // Once all partials are written, one thread counts the unit (releasing the whole CTA's writes,
+      // which the meeting put before it); the last unit's CTA reads them through L2.
       if (!epi_sync()) return false;
       if (threadIdx.x == kEpiFirst * 32) {
-        __threadfence();
-        const int old = atomicAdd(&p.unit_ctr[m_tile * CG + static_cast<int>(rank)], 1);
-        __threadfence();
+        const int old = count_unit(&p.unit_ctr[m_tile * CG + static_cast<int>(rank)]);
         *sm.last_flag = old == units - 1 ? 1 : 0;
       }
       if (!epi_sync()) return false;

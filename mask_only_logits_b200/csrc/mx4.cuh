@@ -143,7 +143,7 @@ __device__ __forceinline__ void quantize_piece(const T* src, int k0, int K, int 
 }
 
 // X [rows, K] (row stride ld elements) to MXFP4: a warp per row, piece by piece.  Bound by HBM:
-// 2.53 bytes move per bf16 element (126464 x 4096: 218 us, 6.0 TB/s).  kGridPerSm CTAs per SM: a
+// 2.53 bytes move per bf16 element (126464 x 4096: 211 us, 6.2 TB/s).  kGridPerSm CTAs per SM: a
 // grid of the 4 to 8 that are resident at once, each with many rows, took 12% longer.
 template <typename T>
 __global__ void __launch_bounds__(kThreads)

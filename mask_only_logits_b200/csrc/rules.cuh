@@ -344,7 +344,8 @@ token_count_kernel(const int* __restrict__ tokens, const uint8_t* __restrict__ M
   }
   const long long row = static_cast<long long>(b) * n;
   const int v1 = v0 + slice < V ? v0 + slice : V;
-  for (int j = threadIdx.x; j < valid; j += kCountThreads) {
+  // unsigned: n may be 2^31 - 1, and j goes a stride past it
+  for (unsigned j = threadIdx.x; j < static_cast<unsigned>(valid); j += kCountThreads) {
     if (M && M[row + j] != 0) continue;
     const int t = tokens[row + j];
     if (t >= v0 && t < v1) atomicAdd(&hist[t - v0], 1);
@@ -368,10 +369,10 @@ token_add_kernel(const int* __restrict__ tokens, const uint8_t* __restrict__ M,
   pdl_wait();
   pdl_launch_dependents();
   const int b = blockIdx.y;
-  const int valid = n_valid ? (n_valid[b] < n ? n_valid[b] : n) : n;
+  const unsigned valid = n_valid ? min(max(n_valid[b], 0), n) : n;
   const long long row = static_cast<long long>(b) * n;
   const int words = (V + 31) / 32;
-  for (int j = blockIdx.x * kCountThreads + threadIdx.x; j < valid; j += gridDim.x * kCountThreads) {
+  for (unsigned j = blockIdx.x * kCountThreads + threadIdx.x; j < valid; j += gridDim.x * kCountThreads) {
     if (M && M[row + j] != 0) continue;
     const int t = tokens[row + j];
     if (t < 0 || t >= V) continue;

@@ -61,6 +61,23 @@ def test_token_counts(dl, B, n, V, masked):
     np.testing.assert_array_equal(seen.cpu().numpy(), S.pack_bits(ref > 0))
 
 
+def test_token_counts_of_the_longest_sequence(dl):
+    """n = 2^31 - 1: strides past the last token stay ahead of 31 bits."""
+    n, V = 2**31 - 1, 70
+    tokens = torch.full((1, n), -1, dtype=torch.int32, device="cuda")
+    at = [0, 511, 2**31 - 37000, n - 300, n - 1]
+    for v, j in enumerate(at):
+        tokens[0, j] = v
+    counts, seen = i32(1, V), i32(1, (V + 31) // 32)
+    dl.token_counts(tokens, counts, seen)
+    dl.token_counts(tokens, counts, seen, accumulate=True)
+    ref = torch.zeros(1, V, dtype=torch.int32)
+    ref[0, :len(at)] = 2
+    assert dl.get_status() == 0
+    assert torch.equal(counts.cpu(), ref)
+    assert seen.cpu().tolist() == [[2**len(at) - 1, 0, 0]]
+
+
 # ---------------------------------------------------------------------------------------
 # MXFP4
 # ---------------------------------------------------------------------------------------

@@ -939,6 +939,7 @@ class DecodeStep:
         with torch.cuda.graph(graph, capture_error_mode="thread_local"):
             self.run(H, M, W, win_lo, win_hi, None, block_only, rules=rules)
         self._graph = graph
+        self._graph_rules = rules                # its tensors live as long as the graph does
         return graph
 
     def replay(self, stream=None) -> dict:

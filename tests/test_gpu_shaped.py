@@ -572,6 +572,24 @@ def test_capture_other_stream_and_host_inputs(dl, weights):
     assert dl.get_status() == 0
 
 
+def test_captured_step_keeps_its_rules(dl):
+    """Rules that nothing but the graph refers to: their tensors are not given to others."""
+    B, L, d, V, k = 1, 40, 64, 500, 4
+    H, M, W = (t.cuda() for t in head_inputs(B, L, d, V, "half", seed=9))
+
+    def rules():
+        bias = torch.zeros(V, device="cuda")
+        bias[123] = 1000.0
+        return dl.LogitRules(B, L, V, bias=bias)
+
+    step = dl.DecodeStep(B, L, d, V, k)
+    step.capture(H, M, W, rules=rules())
+    junk = [torch.full((V,), float(i), device="cuda") for i in range(64)]
+    c = int(step.replay()["count"][0])
+    assert c > 0 and step.tok[:c].tolist() == [123] * c
+    assert len(junk) == 64 and dl.get_status() == 0
+
+
 def test_two_steps_on_two_streams(dl):
     """Two steps at once, each with its own buffers and rules, on two streams."""
     B, L, d, V = 1, 200, 256, 3000

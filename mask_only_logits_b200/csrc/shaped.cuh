@@ -22,7 +22,7 @@
 //   A rows    single CTAs load their rows of Hm in boxes of 32, only as many as are masked; the
 //             rest of the operand's 128 rows is zeroed once: the tensor cores' power depends on
 //             what they multiply, and streaming W for one row runs at the power cap (one row
-//             d4096 V126464, back to back: bf16 195.3 -> 191.8 us, MXFP4 65.4 -> 64.4 us).
+//             d4096 V126464, back to back: bf16, K in pieces of 512, 195.3 -> 191.8 us, MXFP4 65.4 -> 64.4 us).
 //   order     the schedule's vocabulary tile i is tile i * step mod (tiles), step coprime to the
 //             tiles and about 0.62 of them: frequent tokens sit at the low ids of a vocabulary,
 //             so a stream of consecutive tiles would get all the penalised columns (99 us where
@@ -31,7 +31,7 @@
 //             towards zero: over d = 4096 a large bf16 logit came out 5e-6 too small.  An
 //             accumulator therefore holds a piece of K; the epilogue adds the pieces up in
 //             registers (128 a thread, dealt to the epilogue's warpgroups by setmaxnreg), which
-//             leaves 0.6e-6 to 1.4e-6, about an fp32 sum's error.  MXFP4 products are a few bits wide and their sums exact.
+//             leaves about an fp32 sum's error (0.1e-6 to 1.4e-6).  MXFP4 products are a few bits wide and their sums exact.
 //   epilogue  eight warps: two per TMEM lane quadrant, each with half of a tile's columns (the
 //             rules and scores cost more instructions than the plain statistics, and four MXFP4
 //             tiles take the time of one bf16 tile).  rules on each 32 logits, then
@@ -358,15 +358,18 @@ __device__ __forceinline__ void run(uint8_t* smem_raw, const Maps& tm, int count
   const Plan pl = Plan::make(count, plan_v<Op>(p.V), static_cast<int>(gridDim.x) / CG, C::kGroupM, C::BM);
   const int holder = static_cast<int>(blockIdx.x) / CG;
   const int KB = (p.d + Op::BK - 1) / Op::BK;
-  // Stages summed in one accumulator (bf16; MXFP4 a tile's whole K).  Single CTAs: 512 of K; W's
-  // way from HBM hides the epilogue's extra reads (one row d4096 V126464: 179 us, unsplit 173).
+  // Stages summed in one accumulator (bf16; MXFP4 a tile's whole K).  Single CTAs: 128 of K; W's
+  // way from HBM hides most of the epilogue's extra reads (one row d4096 V126464: 192 us, with 256
+  // of K 185, with 512 178, unsplit 173), and a call on few rows has no others for its error to
+  // average with: of 40 random calls of 1 to 128 rows 5 came out more than 1e-6 off (256: 8, 512:
+  // 13), as many as with plain fp32 sums.
   // Pairs: a quarter of K, at least 512: with it the error stays by that of an fp32 sum, which
   // grows with K too.  256 rows d2048 V151936 with all rules: 512 219 us, 768 209, 1024 188,
   // unsplit 173; 1024 rows d4096 V126464: 907, 876, 832, 800 us (both under the power cap).
   int piece_stages = KB;
   if (!Op::kMx4) {
     const int quarter = (KB + 3) / 4;
-    const int most = CG == 1 || quarter < 8 ? 8 : quarter;
+    const int most = CG == 1 ? 2 : (quarter < 8 ? 8 : quarter);
     const int pieces = (KB + most - 1) / most;
     piece_stages = (KB + pieces - 1) / pieces;
   }

@@ -22,7 +22,8 @@
 //   A rows    single CTAs load their rows of Hm in boxes of 32, only as many as are masked; the
 //             rest of the operand's 128 rows is zeroed once: the tensor cores' power depends on
 //             what they multiply, and streaming W for one row runs at the power cap (one row
-//             d4096 V126464, back to back: bf16, K in pieces of 512, 195.3 -> 191.8 us, MXFP4 65.4 -> 64.4 us).
+//             d4096 V126464, back to back: bf16, K in pieces of 512, 195.3 -> 191.8 us, MXFP4
+//             65.4 -> 64.4 us).
 //   order     the schedule's vocabulary tile i is tile i * step mod (tiles), step coprime to the
 //             tiles and about 0.62 of them: frequent tokens sit at the low ids of a vocabulary,
 //             so a stream of consecutive tiles would get all the penalised columns (99 us where
@@ -31,7 +32,8 @@
 //             towards zero: over d = 4096 a large bf16 logit came out 5e-6 too small.  An
 //             accumulator therefore holds a piece of K; the epilogue adds the pieces up in
 //             registers (128 a thread, dealt to the epilogue's warpgroups by setmaxnreg), which
-//             leaves about an fp32 sum's error (0.1e-6 to 1.4e-6).  MXFP4 products are a few bits wide and their sums exact.
+//             leaves about an fp32 sum's error (0.1e-6 to 1.4e-6).  MXFP4 products are a few
+//             bits wide and their sums exact.
 //   epilogue  eight warps: two per TMEM lane quadrant, each with half of a tile's columns (the
 //             rules and scores cost more instructions than the plain statistics, and four MXFP4
 //             tiles take the time of one bf16 tile).  rules on each 32 logits, then

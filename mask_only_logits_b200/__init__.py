@@ -17,6 +17,7 @@ device tensors (``run``) or on host tensors with the copies included (``run_host
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 import torch
@@ -645,6 +646,29 @@ def mx4_row_scales(s: torch.Tensor, rows: int, cols: int) -> torch.Tensor:
     return full[:rows, :cols // 32].contiguous()
 
 
+@contextlib.contextmanager
+def _owned_by(stream, *inputs):
+    """For a call that makes its own results on `stream`: what is allocated inside comes from that
+    stream's memory, so that nothing queued on the current stream still uses it, and each tensor
+    passed through the yielded function also stays allocated for what the current stream has
+    queued when it is dropped there.  The inputs stay allocated until `stream` has read them."""
+    if stream is None:
+        yield lambda t: t
+        return
+    here = torch.cuda.current_stream(inputs[0].device)
+    there = stream if hasattr(stream, "cuda_stream") else \
+        torch.cuda.ExternalStream(int(stream), device=inputs[0].device)
+    for t in inputs:
+        t.record_stream(there)
+
+    def own(t):
+        t.record_stream(here)
+        return t
+
+    with torch.cuda.stream(there):
+        yield own
+
+
 class Mx4Matrix:
     """An MXFP4 matrix [rows, cols] on the GPU: codes ``q`` uint8 [rows, cols / 2] and scales
     ``s`` uint8 (the library's tiles).  ``quantize`` makes one from a dense matrix."""
@@ -664,14 +688,19 @@ class Mx4Matrix:
 
     @classmethod
     def quantize(cls, X: torch.Tensor, stream=None) -> "Mx4Matrix":
+        """X [rows, cols] in MXFP4, on the given (or the current) stream: X must be ready there, and
+        other streams wait for it before they use the result."""
         rows, cols = X.shape
-        q = torch.empty(rows, cols // 2, dtype=torch.uint8, device=X.device)
-        s = torch.empty(-(-rows // 128) * -(-cols // 128) * 512, dtype=torch.uint8, device=X.device)
+        with _owned_by(stream, X) as own:
+            q = own(torch.empty(rows, cols // 2, dtype=torch.uint8, device=X.device))
+            s = own(torch.empty(-(-rows // 128) * -(-cols // 128) * 512, dtype=torch.uint8, device=X.device))
         mx4_quantize(X, q, s, stream)
         return cls(q, s)
 
     def dequantize(self, dtype=torch.bfloat16, stream=None) -> torch.Tensor:
-        X = torch.empty(self.rows, self.cols, dtype=dtype, device=self.q.device)
+        """The values the matrix stands for, on the given (or the current) stream."""
+        with _owned_by(stream, self.q, self.s) as own:
+            X = own(torch.empty(self.rows, self.cols, dtype=dtype, device=self.q.device))
         mx4_dequantize(self.q, self.s, X, stream)
         return X
 

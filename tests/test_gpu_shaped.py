@@ -648,3 +648,39 @@ def test_unarmed_stage_times_out(dl, mx4, variant):
     call(dl, mx4, Hd, Md, Wd, rules, 0, o, ws)
     assert dl.get_status() == 0
     check(o, reference(H, M, W, mx4, ref_rules), V, 0)
+
+
+# ---------------------------------------------------------------------------------------
+# buffers that the package makes itself
+# ---------------------------------------------------------------------------------------
+@pytest.mark.parametrize("handle", [False, True], ids=["stream", "handle"])
+def test_mx4_matrix_on_another_stream(dl, handle):
+    """Quantising and dequantising on a side stream leave alone what the current stream still reads
+    of memory given back to the allocator, and what it gets of theirs when they are dropped."""
+    R, K = 8192, 4096
+    side = torch.cuda.Stream()
+    on = side.cuda_stream if handle else side
+    X = torch.randn(R, K, device="cuda", dtype=torch.bfloat16)
+    want = dl.Mx4Matrix.quantize(X)
+    back = want.dequantize()
+    kept = [torch.empty(R, K // 2, dtype=torch.uint8, device="cuda"), torch.empty_like(X)]
+    torch.cuda.synchronize()
+    # memory of the results' sizes, given back while the current stream has yet to read it
+    old = [torch.full_like(kept[0], 7), torch.full_like(kept[1], 7)]
+    torch.cuda._sleep(100_000_000)
+    for k, o in zip(kept, old):
+        k.copy_(o)
+    del old, o
+    got = dl.Mx4Matrix.quantize(X, stream=on)
+    again = got.dequantize(stream=on)
+    torch.cuda.synchronize()
+    assert (kept[0] == 7).all() and (kept[1] == 7).all()
+    assert torch.equal(got.q, want.q) and torch.equal(got.s, want.s) and torch.equal(again, back)
+    # results dropped before the side stream has written them
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)
+    dl.Mx4Matrix.quantize(X, stream=on).dequantize(stream=on)
+    new = [torch.full_like(kept[0], 9), torch.full_like(kept[1], 9)]
+    torch.cuda.synchronize()
+    assert (new[0] == 9).all() and (new[1] == 9).all()
+    assert dl.get_status() == 0

@@ -247,3 +247,42 @@ def test_mx4_workspace_arithmetic(lib):
         assert cap(b, l, dd, v, size(b, l, dd, v, 1) - 1) == 0
         assert cap(b, l, dd, v, 1 << 60) == b * l
     assert size(1, 8, 100, 10, 1) == 0 and size(1, 8, 64, 10, 0) == 0 and cap(1, 8, 100, 10, 1 << 20) == 0
+
+
+def test_mx4_matrix_on_another_stream_owns_its_buffers(fake, monkeypatch):   # noqa: F811
+    """Buffers that a call on `stream` makes come from that stream's memory and stay allocated for
+    the current stream too; what it reads stays allocated until `stream` is done."""
+    class Stream:
+        def __init__(self, handle):
+            self.cuda_stream = handle
+
+        def __enter__(self):
+            active.append(self)
+
+        def __exit__(self, *_):
+            active.pop()
+
+    here, side = Stream(1), Stream(2)
+    active, made, kept = [here], [], []
+    empty = torch.empty
+
+    def logged_empty(*a, **kw):
+        t = empty(*a, **kw)
+        made.append((t.data_ptr(), active[-1]))
+        return t
+
+    monkeypatch.setattr(torch, "empty", logged_empty)
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: s)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: active[-1])
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: kept.append((t.data_ptr(), s)))
+    X = torch.zeros(130, 64, dtype=torch.bfloat16)
+    W = dl.Mx4Matrix.quantize(X, stream=side)
+    q, s = W.q.data_ptr(), W.s.data_ptr()
+    assert made == [(q, side), (s, side)]
+    assert set(kept) == {(X.data_ptr(), side), (q, here), (s, here)}
+    made.clear()
+    kept.clear()
+    Y = W.dequantize(stream=side)
+    assert made == [(Y.data_ptr(), side)]
+    assert set(kept) == {(q, side), (s, side), (Y.data_ptr(), here)}
+    assert fake.calls == ["dllm_mx4_quantize", "dllm_mx4_dequantize"] and active == [here]

@@ -953,7 +953,8 @@ class DecodeStep:
         reruns the whole step (every kernel, with the programmatic-launch edges between them)
         on whatever those tensors hold at replay time, for one launch of CPU work; the
         outputs are this object's buffers as after ``run``.  Tensors must keep their
-        addresses while the graph is used."""
+        addresses while the graph is used; the returned graph holds on to them, and stays
+        valid when another step is captured (``replay()`` then reruns that one)."""
         if self.arena is not None:
             # a graph would keep the workspace size of capture time while the arena's mapping
             # follows later masks
@@ -967,8 +968,9 @@ class DecodeStep:
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph, capture_error_mode="thread_local"):
             self.run(H, M, W, win_lo, win_hi, None, block_only, rules=rules)
+        # what the kernels read lives as long as this graph does, also after a later capture
+        graph.inputs = (H, M, W, win_lo, win_hi, rules)
         self._graph = graph
-        self._graph_rules = rules                # its tensors live as long as the graph does
         return graph
 
     def replay(self, stream=None) -> dict:

@@ -684,3 +684,25 @@ def test_mx4_matrix_on_another_stream(dl, handle):
     torch.cuda.synchronize()
     assert (new[0] == 9).all() and (new[1] == 9).all()
     assert dl.get_status() == 0
+
+
+@pytest.mark.parametrize("weights", ["bf16", "mx4"])
+def test_an_earlier_graph_stays_valid(dl, weights):
+    """Two captures of one step with rules and weights that only the graphs refer to: each graph
+    replays its own."""
+    B, L, d, V, k = 1, 40, 64, 500, 4
+    H, M, W = (t.cuda() for t in head_inputs(B, L, d, V, "half", seed=9))
+    step = dl.DecodeStep(B, L, d, V, k, weights=weights)
+    graphs = []
+    for best in (123, 321):
+        bias = torch.zeros(V, device="cuda")
+        bias[best] = 1000.0
+        Wd = dl.Mx4Matrix.quantize(W) if weights == "mx4" else W.clone()
+        graphs.append(step.capture(H, M, Wd, rules=dl.LogitRules(B, L, V, bias=bias)))
+        del Wd, bias
+    junk = [torch.full((n,), float(i), device="cuda") for i in range(64) for n in (V, V * d // 4)]
+    for g, best in zip(graphs + graphs[:1], (123, 321, 123)):
+        g.replay()
+        c = int(step.count[0])
+        assert c > 0 and step.tok[:c].tolist() == [best] * c
+    assert len(junk) == 128 and dl.get_status() == 0

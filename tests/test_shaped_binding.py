@@ -286,3 +286,36 @@ def test_mx4_matrix_on_another_stream_owns_its_buffers(fake, monkeypatch):   # n
     assert made == [(Y.data_ptr(), side)]
     assert set(kept) == {(q, side), (s, side), (Y.data_ptr(), here)}
     assert fake.calls == ["dllm_mx4_quantize", "dllm_mx4_dequantize"] and active == [here]
+
+
+def test_each_captured_graph_keeps_what_it_reads(fake, monkeypatch):      # noqa: F811
+    """Two captures of one step: the first graph still holds its own rules and tensors."""
+    import contextlib
+    import gc
+    import weakref
+
+    class Stream:
+        cuda_stream = 1
+
+        def wait_stream(self, other):
+            pass
+
+    class Graph:
+        pass
+
+    monkeypatch.setattr(torch.cuda, "Stream", lambda *a: Stream())
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: Stream())
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
+    monkeypatch.setattr(torch.cuda, "CUDAGraph", Graph)
+    monkeypatch.setattr(torch.cuda, "graph", lambda g, **kw: contextlib.nullcontext())
+    b = bufs()
+    step = dl.DecodeStep(B, L, d, V, 4, device="cpu")
+    bias = [torch.zeros(V), torch.zeros(V)]
+    refs = [weakref.ref(t) for t in bias]
+    graphs = [step.capture(b["H"], b["M"], b["W"], rules=dl.LogitRules(B, L, V, bias=t)) for t in bias]
+    del bias
+    gc.collect()
+    assert all(r() is not None for r in refs)
+    del graphs[0]
+    gc.collect()
+    assert refs[0]() is None and refs[1]() is not None    # and no longer than that

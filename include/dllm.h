@@ -391,7 +391,7 @@ dllm_status dllm_lse_merge(const float* part_m, const float* part_s, const int32
  * For each sequence b, the candidates are its masked positions l = row_idx[i] - b*L for
  * i in [seq_off[b], seq_off[b+1]), restricted to win_lo[b] <= l < win_hi[b] when windows
  * are given.  The k candidates of largest conf are selected, ordered by conf descending,
- * then by position ascending (this order also breaks exact ties).
+ * then by position ascending (this order also breaks exact ties; -0 orders below +0).
  *
  *   conf, row_idx, seq_off   device, as produced by dllm_masked_logits (compacted order).
  *   win_lo, win_hi   device int32 [B] or both NULL (no window).

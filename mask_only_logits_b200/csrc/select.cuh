@@ -12,8 +12,8 @@
 //     (order-preserving bits of score[r]) << 32 | ~r
 // Order-preserving bits: a float's IEEE bits with the sign bit flipped, or all bits flipped
 // for negative values, compare as unsigned integers like the floats (scores may be negative,
-// e.g. minus an entropy).  Within a sequence r ascends with the position, so ~r puts the
-// lower position first among equal scores.
+// e.g. minus an entropy; -0 is below +0).  Within a sequence r ascends with the position, so
+// ~r puts the lower position first among equal scores.
 // Steps:
 //   1. candidate range: rows of the sequence whose position lies in the window (one pass:
 //      the window's rows are contiguous because row_idx ascends); with a threshold, the
@@ -112,7 +112,8 @@ select_unmask_kernel(const float* __restrict__ conf, const int* __restrict__ row
   if (use_threshold) {
     if (tid == 0) sh_q = 0;
     __syncthreads();
-    const uint32_t tq = okey(threshold);
+    // zeros are equal to a threshold whatever their signs (only their order differs)
+    const uint32_t tq = okey(threshold == 0.f ? (ascending ? 0.f : -0.f) : threshold);
     int mine = 0;
 #pragma unroll 8
     for (int r = c0 + tid; r < c1; r += kSelThreads) mine += key_of(r) >= tq ? 1 : 0;

@@ -706,3 +706,21 @@ def test_an_earlier_graph_stays_valid(dl, weights):
         c = int(step.count[0])
         assert c > 0 and step.tok[:c].tolist() == [best] * c
     assert len(junk) == 128 and dl.get_status() == 0
+
+
+@pytest.mark.parametrize("n", [5, 300, 5000])
+@pytest.mark.parametrize("ascending", [False, True])
+def test_a_threshold_of_zero_takes_zeros_of_either_sign(dl, ascending, n):
+    """Scores at least as good as the threshold in the numbers' order, where zeros are equal."""
+    rng = np.random.default_rng(n)
+    score = rng.choice(np.float32([-1.0, -0.0, 0.0, 1.0]), n)
+    passing = int((score <= 0).sum() if ascending else (score >= 0).sum())
+    for tau in (0.0, -0.0):
+        idx, n_sel = i32(1, 1024), i32(1)
+        dl.select_unmask_ex(torch.from_numpy(score).cuda(), torch.arange(n, dtype=torch.int32, device="cuda"),
+                            torch.tensor([0, n], dtype=torch.int32, device="cuda"), 1, n, 1024, tau, 0, idx,
+                            n_sel, ascending)
+        assert int(n_sel[0]) == min(passing, 1024), tau
+        taken = idx[0, :int(n_sel[0])].cpu().numpy()
+        assert (score[taken] <= 0).all() if ascending else (score[taken] >= 0).all()
+    assert dl.get_status() == 0

@@ -490,7 +490,8 @@ dllm_status dllm_decode_block_step(const uint16_t* H, const uint8_t* M, const ui
  *               (allow_rows == B).
  *
  * A row with no token left (every z = -infinity): tok = -1, conf = 0, lse = -infinity,
- * entropy = +infinity, margin = 0.  A selection takes such a row after all others.
+ * entropy = +infinity, margin = -0.  A selection by one of these scores takes such a row after
+ * all others (a row whose two best logits are equal has margin +0, which orders above -0).
  */
 typedef struct dllm_logit_rules {
   const float* bias;

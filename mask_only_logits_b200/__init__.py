@@ -577,7 +577,8 @@ def _logits_args(H, M, d, tok, conf, lse, entropy, margin, row_idx, seq_off, cou
 def masked_logits_rules(H, M, W, rules: LogitRules, stats, tok, conf, lse, entropy, margin, row_idx,
                         seq_off, count, ws, stream=None, win_lo=None, win_hi=None) -> None:
     """masked_logits_ex with rules on the logits (applied in the GEMM epilogue).  A row with no
-    token left gets tok -1, conf 0, lse -inf, entropy +inf, margin 0."""
+    token left gets tok -1, conf 0, lse -inf, entropy +inf, margin -0 (a
+    selection puts it behind the +0 of two equal best logits)."""
     B, L = M.shape
     V, d = W.shape
     dev = _call_device(count)

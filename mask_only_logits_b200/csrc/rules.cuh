@@ -297,8 +297,9 @@ __device__ __forceinline__ void merge(lm::RowState& st, float m, float s, int a,
 }
 
 // Final values of a row.  Nothing allowed: no token, no confidence, and the worst of each
-// score, so that a selection takes such a row last.  A row whose every logit is NaN has NaN
-// statistics and token 0.
+// score, so that a selection takes such a row last; the margin is a negative zero, behind the zero
+// of a row whose two best logits are equal.  A row whose every logit is NaN has NaN statistics and
+// token 0.
 __device__ __forceinline__ void finish(const lm::RowState& st, int& tok, float& conf, float& lse,
                                        float& ent, float& margin) {
   if (st.m == -INFINITY && st.s == 0.f) {
@@ -306,7 +307,7 @@ __device__ __forceinline__ void finish(const lm::RowState& st, int& tok, float& 
     conf = 0.f;
     lse = -INFINITY;
     ent = INFINITY;
-    margin = 0.f;
+    margin = -0.f;
     return;
   }
   const float ls = logf(st.s);

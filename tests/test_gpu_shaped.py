@@ -708,6 +708,36 @@ def test_an_earlier_graph_stays_valid(dl, weights):
     assert len(junk) == 128 and dl.get_status() == 0
 
 
+# ---------------------------------------------------------------------------------------
+# rows that no token is left for, in a selection
+# ---------------------------------------------------------------------------------------
+@pytest.mark.parametrize("n", [40, 300, 5000], ids=["ranked", "staged", "long"])
+@pytest.mark.parametrize("policy", ["confidence", "entropy", "margin"])
+@pytest.mark.parametrize("weights", ["bf16", "mx4"])
+def test_rows_without_a_token_come_last(dl, weights, policy, n):
+    """Every second position may take nothing, and all logits of the others are equal (margin 0,
+    the least confidence): a selection of as many as can be filled takes those, in order, and a
+    selection of more the others after them.  n: each of the selection's ways."""
+    L, d, V = n, 64, 40
+    H = torch.zeros(L, d, dtype=torch.bfloat16, device="cuda")
+    W = torch.zeros(V, d, dtype=torch.bfloat16, device="cuda")
+    M = torch.ones(1, L, dtype=torch.uint8, device="cuda")
+    allow = torch.from_numpy(S.pack_bits(np.stack([np.zeros(V, bool), np.ones(V, bool)]))).cuda()
+    ids = (torch.arange(L, dtype=torch.int32, device="cuda") % 2)[None].contiguous()
+    rules = dl.LogitRules(1, L, V, allow=allow, allow_id=ids)
+    Wd = dl.Mx4Matrix.quantize(W) if weights == "mx4" else W
+    full = list(range(1, L, 2))
+    for k, threshold in ((L // 2, None), (L // 2 + 7, None),
+                         (L // 2 + 7, dict(confidence=0.0, entropy=np.inf, margin=0.0)[policy])):
+        k = min(k, dl.MAX_K)
+        step = dl.DecodeStep(1, L, d, V, k, policy=policy, threshold=threshold, weights=weights)
+        out = step.run(H, M, Wd, rules=rules)
+        assert dl.get_status() == 0 and int(out["n_sel"][0]) == k
+        want = (full + [0, 2, 4, 6, 8, 10, 12])[:k]
+        assert out["idx"][0].tolist() == want
+        assert out["tok_sel"][0].tolist() == [0 if l % 2 else -1 for l in want]
+
+
 @pytest.mark.parametrize("n", [5, 300, 5000])
 @pytest.mark.parametrize("ascending", [False, True])
 def test_a_threshold_of_zero_takes_zeros_of_either_sign(dl, ascending, n):

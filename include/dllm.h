@@ -76,7 +76,8 @@ typedef int32_t dllm_status;
 #define DLLM_ERR_WORKSPACE  -4   /* workspace too small (see dllm_workspace_bytes_rows)      */
 #define DLLM_ERR_CUDA       -5   /* a CUDA runtime/driver call failed                       */
 #define DLLM_ERR_TIMEOUT    -6   /* a device-side wait exceeded its limit (kernel returned) */
-#define DLLM_ERR_DEVICE     -7   /* the current device is not an sm_100 GPU                 */
+#define DLLM_ERR_DEVICE     -7   /* the current device is not an sm_100 GPU, or this build of
+                                    a kernel does not fit it (dllm_masked_logits_rules)     */
 #define DLLM_ERR_BOUNDS     -8   /* a device-side bound check failed (access skipped)       */
 #define DLLM_ERR_SCRATCH    -9   /* B*L exceeds the fixed scratch of dllm_mask_compact_noalloc */
 #define DLLM_ERR_MEMORY     -10  /* an input is neither device memory nor page-locked host memory */
@@ -517,7 +518,8 @@ typedef struct dllm_logit_rules {
  * DLLM_ERR_NULL (counts without seen or seen without counts, a penalty without counts,
  * allow_id without allow), DLLM_ERR_ALIGN (a pointer that is not 16-byte aligned),
  * DLLM_ERR_SHAPE (V > 2^30, a stride too small, bias_stride not a multiple of 4, allow_rows < 1
- * or, without allow_id, neither 1 nor B).
+ * or, without allow_id, neither 1 nor B), DLLM_ERR_DEVICE (also where the
+ * library was compiled to another register count than the bf16 kernel's warps share out).
  */
 dllm_status dllm_masked_logits_rules(const uint16_t* H, const uint8_t* M, const uint16_t* W,
                                      int32_t B, int32_t L, int32_t d, int32_t V,

@@ -54,6 +54,7 @@ struct DeviceState {
   dllm_status err = DLLM_OK;
   int sms = 0;
   int pairs = 0;                // co-resident CTA pairs of the cta_group::2 GEMM
+  bool shaped_bf16 = false;     // the bf16 kernels of shaped.cuh may run (see device_state)
   int* status = nullptr;        // device address of g_status on this device
 };
 
@@ -171,14 +172,14 @@ dllm_status device_state(DeviceState** out) {
            cudaFuncSetAttribute(rules::token_count_kernel, smem_attr, rules::kCountMaxSlice * 4)))
         st.err = DLLM_ERR_CUDA;
       // the bf16 kernels of shaped.cuh deal their registers out anew: what the warpgroups take must be
-      // what the launch gave them, or they would wait for the rest
+      // what the launch gave them, or they would wait for the rest.  In a build that gives them
+      // another number the calls that launch them are refused, and no others.
       cudaFuncAttributes fa0, fa1;
       if (st.err == DLLM_OK &&
           (cudaFuncGetAttributes(&fa0, shaped::shaped_kernel<shaped::Bf16, true, false>) ||
            cudaFuncGetAttributes(&fa1, shaped::shaped_kernel<shaped::Bf16, true, true>)))
         st.err = DLLM_ERR_CUDA;
-      if (st.err == DLLM_OK && (fa0.numRegs != shaped::kLaunchRegs || fa1.numRegs != shaped::kLaunchRegs))
-        st.err = DLLM_ERR_DEVICE;
+      st.shaped_bf16 = st.err == DLLM_OK && fa0.numRegs == shaped::kLaunchRegs && fa1.numRegs == shaped::kLaunchRegs;
       if (st.err == DLLM_OK) {
         // how many CTA pairs of the paired GEMM can be resident at once (a persistent grid
         // larger than that would serialise)
@@ -581,7 +582,6 @@ template <class Op>
 dllm_status launch_shaped(const ShapedArgs& x, const DeviceState& ds, const WsLayout& w,
                           const lm::Outputs& outs) {
   const LogitsArgs& a = x.a;
-  if (ds.pairs < 1) return DLLM_ERR_DEVICE;
   uint8_t* ws = static_cast<uint8_t*>(a.ws);
   const void* Hm = ws + w.hm_off;
   const uint64_t n = static_cast<uint64_t>(w.rows), V = static_cast<uint64_t>(a.V);
@@ -711,6 +711,7 @@ dllm_status run_shaped(const ShapedArgs& x) {
   if (w.rows < 1) return DLLM_ERR_WORKSPACE;
   DeviceState* ds = nullptr;
   if ((st = device_state(&ds)) != DLLM_OK) return st;
+  if (ds->pairs < 1 || (!mx4 && !ds->shaped_bf16)) return DLLM_ERR_DEVICE;
   if ((st = stage_shaped(a, *ds, w, mx4)) != DLLM_OK) return st;
   const lm::Outputs outs{a.tok, a.conf, a.lse, a.entropy, a.margin, a.raw, 0};
   return mx4 ? launch_shaped<shaped::Mx4>(x, *ds, w, outs) : launch_shaped<shaped::Bf16>(x, *ds, w, outs);
@@ -808,7 +809,7 @@ const char* dllm_status_string(dllm_status s) {
     case DLLM_ERR_WORKSPACE: return "workspace too small";
     case DLLM_ERR_CUDA: return "CUDA error";
     case DLLM_ERR_TIMEOUT: return "a device-side wait timed out";
-    case DLLM_ERR_DEVICE: return "device is not an sm_100 GPU";
+    case DLLM_ERR_DEVICE: return "device is not an sm_100 GPU, or the library was not built for it";
     case DLLM_ERR_BOUNDS: return "a device-side bound check failed";
     case DLLM_ERR_SCRATCH: return "B*L exceeds the fixed scratch of the allocation-free entry point";
     case DLLM_ERR_MEMORY: return "an input is neither device memory nor page-locked host memory";

@@ -169,7 +169,10 @@ __device__ __forceinline__ uint64_t scale_desc(uint32_t smem_addr) {
 
 // Registers of a thread, moved between the warpgroups of a CTA (bf16): 384 threads start with
 // kLaunchRegs each (the host checks that the build has them).
-constexpr int kLaunchRegs = 168, kProducerRegs = 72, kEpilogueRegs = 216;
+#ifndef DLLM_SHAPED_LAUNCH_REGS
+#define DLLM_SHAPED_LAUNCH_REGS 168                  // other values: a test of the host's check
+#endif
+constexpr int kLaunchRegs = DLLM_SHAPED_LAUNCH_REGS, kProducerRegs = 72, kEpilogueRegs = 216;
 static_assert(kProducerRegs + 2 * kEpilogueRegs <= 3 * kLaunchRegs, "more registers than the launch has");
 template <int N>
 __device__ __forceinline__ void give_registers() {

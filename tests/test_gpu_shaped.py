@@ -754,3 +754,40 @@ def test_a_threshold_of_zero_takes_zeros_of_either_sign(dl, ascending, n):
         taken = idx[0, :int(n_sel[0])].cpu().numpy()
         assert (score[taken] <= 0).all() if ascending else (score[taken] >= 0).all()
     assert dl.get_status() == 0
+
+
+# ---------------------------------------------------------------------------------------
+# a build whose registers do not fit
+# ---------------------------------------------------------------------------------------
+def test_a_build_with_other_registers_refuses_one_kernel_only(dl):
+    """A copy of the library that expects another register count of the bf16 kernel with rules: that
+    call is refused before anything is launched, and every other one runs."""
+    import os
+
+    from mask_only_logits_b200 import _abi, build
+    out = os.path.join(build.PKG_DIR, "libdllm_other_registers.so")
+    if not os.path.exists(out) or os.path.getmtime(out) < os.path.getmtime(build.LIB_PATH):
+        build.build(extra_flags=["-DDLLM_SHAPED_LAUNCH_REGS=176"], out=out)
+    lib = _abi.load_from(out)
+    B, L, d, V, k = 1, 60, 128, 700, 4
+    H, M, W = head_inputs(B, L, d, V, "half", seed=1)
+    Hd, Md, Wd, Q = H.cuda(), M.cuda(), W.cuda(), dl.Mx4Matrix.quantize(W.cuda())
+    o = outputs(L, B, 0)
+    ws = torch.empty(max(dl.workspace_bytes(B, L, d, V), dl.workspace_bytes_mx4(B, L, d, V)),
+                     dtype=torch.uint8, device="cuda")
+    p = lambda t: ctypes.c_void_p(t.data_ptr())                        # noqa: E731
+    nul, stream = ctypes.c_void_p(None), ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    rules = dl.LogitRules(B, L, V, bias=torch.zeros(V, device="cuda"))._struct
+    tail = [0, p(o["tok"]), p(o["conf"]), p(o["lse"]), nul, nul, p(o["row_idx"]), p(o["seq_off"]),
+            p(o["count"]), p(ws), ws.numel(), stream]
+    dims = [B, L, d, V, nul, nul, ctypes.byref(rules)]
+    assert lib.dllm_masked_logits_rules(p(Hd), p(Md), p(Wd), *dims, *tail) == -7       # DLLM_ERR_DEVICE
+    assert lib.dllm_get_status(stream) == 0 and (o["count"] == -7).all() and (o["tok"] == -7).all()
+    assert lib.dllm_masked_logits_mx4(p(Hd), p(Md), p(Q.q), p(Q.s), *dims, *tail) == 0
+    assert lib.dllm_get_status(stream) == 0
+    check(o, reference(H, M, W, True, {}), V, 0)
+    want = dl.DecodeStep(B, L, d, V, k).run(Hd, Md, Wd)["idx"]
+    idx, n_sel = i32(B, k), i32(4)
+    assert lib.dllm_decode_step(p(Hd), p(Md), p(Wd), B, L, d, V, k, nul, nul, *tail[1:4], *tail[6:9], p(idx),
+                                p(n_sel), nul, nul, p(ws), ws.numel(), stream) == 0
+    assert lib.dllm_get_status(stream) == 0 and torch.equal(idx, want)

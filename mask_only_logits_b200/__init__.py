@@ -469,6 +469,12 @@ def _rows_ptr(t, dtypes, name: str, rows: int, cols: int) -> tuple:
     return t.data_ptr(), ld
 
 
+def _rows_of_width(t: torch.Tensor, n: int, name: str) -> None:
+    """Refuse a matrix whose rows are longer than the n elements that each sequence is read as."""
+    if t.dim() > 1 and t.shape[-1] > n:
+        raise ValueError(f"{name}: expected rows of {n}, got {list(t.shape)}")
+
+
 class LogitRules:
     """Rules on the logits of a step of shape (B, L, V): the tensors and their checked
     description (``dllm_logit_rules``).  For token v at masked position (b, l) with raw logit
@@ -522,6 +528,7 @@ class LogitRules:
             r.allow_rows = allow.shape[0]
             if allow_id is not None:
                 r.allow_id = _ptr(allow_id, torch.int32, "allow_id", n=B * L).value
+                _rows_of_width(allow_id, L, "allow_id")
             elif allow.shape[0] not in (1, B):
                 raise ValueError(f"allow: {allow.shape[0]} bitmaps for {B} sequences need allow_id")
         self._struct = r
@@ -551,6 +558,8 @@ def token_counts(tokens, counts, seen, M=None, n_valid=None, accumulate=False, s
     if seen.dtype is not torch.int32 and seen.dtype is not torch.uint32:
         raise ValueError(f"seen: expected torch.int32, got {seen.dtype}")
     dev = _call_device(counts)
+    if M is not None:
+        _rows_of_width(M, n, "M")
     _check(lib().dllm_token_counts(
         _arg(tokens, torch.int32, "tokens", 0, dev), _arg(M, torch.uint8, "M", B * n, dev),
         _arg(n_valid, torch.int32, "n_valid", B, dev), B, n, V, 1 if accumulate else 0,

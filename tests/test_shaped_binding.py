@@ -319,3 +319,17 @@ def test_each_captured_graph_keeps_what_it_reads(fake, monkeypatch):      # noqa
     del graphs[0]
     gc.collect()
     assert refs[0]() is None and refs[1]() is not None    # and no longer than that
+
+
+def test_rows_of_another_length_are_refused(fake):                       # noqa: F811
+    """A mask or a table of positions with longer rows holds enough elements, but not in the rows
+    that the kernels read; flat ones are taken as they are."""
+    tokens, counts, seen = (torch.zeros(B, 7, dtype=torch.int32), torch.zeros(B, V, dtype=torch.int32),
+                            torch.zeros(B, WORDS, dtype=torch.int32))
+    with pytest.raises(ValueError, match="M: expected rows of 7"):
+        dl.token_counts(tokens, counts, seen, M=torch.zeros(B, 8, dtype=torch.uint8), stream=S)
+    with pytest.raises(ValueError, match="allow_id: expected rows of 40"):
+        dl.LogitRules(B, L, V, **dict(tables(), allow_id=torch.zeros(B, L + 1, dtype=torch.int32)))
+    assert fake.calls == []
+    dl.token_counts(tokens, counts, seen, M=torch.zeros(B * 7, dtype=torch.uint8), stream=S)
+    dl.LogitRules(B, L, V, **dict(tables(), allow_id=torch.zeros(N, dtype=torch.int32)))

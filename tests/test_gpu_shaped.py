@@ -791,3 +791,116 @@ def test_a_build_with_other_registers_refuses_one_kernel_only(dl):
     assert lib.dllm_decode_step(p(Hd), p(Md), p(Wd), B, L, d, V, k, nul, nul, *tail[1:4], *tail[6:9], p(idx),
                                 p(n_sel), nul, nul, p(ws), ws.numel(), stream) == 0
     assert lib.dllm_get_status(stream) == 0 and torch.equal(idx, want)
+
+
+# ---------------------------------------------------------------------------------------
+# accuracy
+# ---------------------------------------------------------------------------------------
+@pytest.mark.parametrize("variant,first", [(1, 128), (2, 1024)], ids=["single", "pair"])
+def test_bf16_sums_are_taken_in_pieces(dl, variant, first):
+    """A product of 16 (or 8), then, from k = first on, products of 2^-24 (2^-25): beside the large
+    one each of them is below fp32's last place and lost, in pieces of their own they add up to
+    multiples of 2^-17 (2^-18), which the large one takes exactly.  So the logit is exact, and the
+    log-sum-exp off by its own rounding, half of 2^-19, and less than 2^-21 for the logarithm;
+    summed in one go it would be 1.8e-4 lower."""
+    d, V, n = 4096, 600, 3 if variant == 1 else 300
+    H, W = torch.zeros(n, d), torch.zeros(V, d)
+    H[:, 0] = W[5, 0] = 4.0
+    H[:, first:] = W[5, first:] = 2.0 ** -12
+    H[1::2] *= 0.5
+    z = 16.0 + (d - first) * 2.0 ** -24
+    z = np.where(np.arange(n) % 2, z / 2, z)
+    o = outputs(n, 1, ALL)
+    ws = torch.empty(dl.workspace_bytes(1, n, d, V), dtype=torch.uint8, device="cuda")
+    rules = dl.LogitRules(1, n, V, bias=torch.zeros(V, device="cuda"))
+    dl.debug_set_gemm_variant(variant)
+    try:
+        call(dl, False, H.bfloat16().cuda(), torch.ones(1, n, dtype=torch.uint8, device="cuda"),
+             W.bfloat16().cuda(), rules, ALL, o, ws)
+        assert dl.get_status() == 0
+    finally:
+        dl.debug_set_gemm_variant(0)
+    lse = z + np.log1p((V - 1) * np.exp(-z))
+    assert (o["tok"] == 5).all()
+    assert np.abs(o["lse"].double().cpu().numpy() - lse).max() <= 2.0 ** -20 + 2.0 ** -21
+
+
+@pytest.mark.parametrize("mx4", [False, True], ids=["bf16", "mx4"])
+@pytest.mark.parametrize("variant,n", [(1, 3), (2, 300)], ids=["single", "pair"])
+def test_every_column_counts_once(dl, mx4, variant, n):
+    """V equal logits: the sum of their exponentials is the number V, exactly, so conf is 1 / V to a
+    rounding (a column lost or counted twice is a hundred of them) and the entropy ln V."""
+    d, V = 64, 151937
+    H, _, _ = head_inputs(1, n, d, 8, "all", seed=3)
+    W = torch.zeros(V, d, dtype=torch.bfloat16, device="cuda")
+    o = outputs(n, 1, ALL)
+    ws = torch.empty(max(dl.workspace_bytes(1, n, d, V), dl.workspace_bytes_mx4(1, n, d, V)),
+                     dtype=torch.uint8, device="cuda")
+    M = torch.ones(1, n, dtype=torch.uint8, device="cuda")
+    for rules in ([None] if mx4 else []) + [dl.LogitRules(1, n, V, bias=torch.full((V,), 2.0, device="cuda"))]:
+        dl.debug_set_gemm_variant(variant)
+        try:
+            call(dl, mx4, H.cuda(), M, dl.Mx4Matrix.quantize(W) if mx4 else W, rules, ALL, o, ws)
+            assert dl.get_status() == 0
+        finally:
+            dl.debug_set_gemm_variant(0)
+        assert (o["tok"] == 0).all() and (o["margin"] == 0).all()
+        np.testing.assert_allclose(o["conf"].double().cpu().numpy(), 1 / V, rtol=2.0 ** -23)
+        # ln V = 11.9: the logarithm's rounding (2^-22 of it at most) and one of the sum with 2
+        np.testing.assert_allclose(o["entropy"].double().cpu().numpy(), np.log(V), rtol=2.0 ** -22)
+        np.testing.assert_allclose(o["lse"].double().cpu().numpy(), np.log(V) + (2.0 if rules else 0.0),
+                                   rtol=2.0 ** -22 + 2.0 ** -24)
+
+
+@pytest.mark.parametrize("variant,n", [(1, 40), (2, 200)], ids=["single", "pair"])
+@pytest.mark.parametrize("span", [(12, 0), (6, 6), (12, 12)], ids=["rows", "both", "wide"])
+def test_mx4_sums_of_blocks_of_very_different_size(dl, span, variant, n):
+    """Blocks of 32 channels whose scales lie up to 2^24 apart, in the rows, in W or in both (outlier
+    channels): such sums do not fit fp32.  Each of the d / 64 tensor-core steps may then cut off the
+    running sum's last place: dz <= d / 64 * 2^-23 * the largest running sum, and the statistics
+    add what check counts."""
+    d, V = 4096, 1030
+    g = torch.Generator().manual_seed(n + span[1])
+    H, W = torch.randn(n, d, generator=g), torch.randn(V, d, generator=g)
+    for t, e in ((H, span[0]), (W, span[1])):
+        t *= torch.exp2(torch.randint(-e, e + 1, (d // 32,), generator=g).float()).repeat_interleave(32)
+    W = (W.double() * (20 / (H.double() @ W.double().T).abs().max())).bfloat16()
+    H = H.bfloat16()
+    h, w = dense(H, True), dense(W, True)
+    z, largest = np.zeros((n, V)), np.zeros(n)
+    for k in range(0, d, 64):
+        z += h[:, k:k + 64] @ w[:, k:k + 64].T
+        largest = np.maximum(largest, np.abs(z).max(-1))
+    r = S.row_stats(z)
+    dz = d // 64 * 2.0 ** -23 * largest
+    r.update(pos=np.arange(n), z=z, dz=dz)
+    o = outputs(n, 1, ALL)
+    ws = torch.empty(dl.workspace_bytes_mx4(1, n, d, V), dtype=torch.uint8, device="cuda")
+    dl.debug_set_gemm_variant(variant)
+    try:
+        call(dl, True, H.cuda(), torch.ones(1, n, dtype=torch.uint8, device="cuda"),
+             dl.Mx4Matrix.quantize(W.cuda()), None, ALL, o, ws)
+        assert dl.get_status() == 0
+    finally:
+        dl.debug_set_gemm_variant(0)
+    check(o, r, 1, ALL)                              # V = 1: no allowance for a plain sum's roundings
+
+
+# ---------------------------------------------------------------------------------------
+# larger problems
+# ---------------------------------------------------------------------------------------
+@pytest.mark.parametrize("mx4", [False, True], ids=["bf16", "mx4"])
+@pytest.mark.parametrize("B,L,d,V", [(2, 2600, 64, 6007),       # two groups of m-tiles, paced
+                                     (1, 300, 2624, 700),       # K in four pieces of 11 stages
+                                     (1, 20, 4160, 520)], ids=["rows", "d2624", "d4160"])
+def test_larger_problems(dl, B, L, d, V, mx4):
+    H, M, W = head_inputs(B, L, d, V, "all", seed=V)
+    ref_rules, dev = make_rules(["penalty", "grammar", "bias"], B, L, V, seed=V)
+    r = reference(H, M, W, mx4, ref_rules)
+    o = outputs(B * L, B, ALL)
+    nbytes = dl.workspace_bytes_mx4(B, L, d, V) if mx4 else dl.workspace_bytes(B, L, d, V)
+    ws = torch.full((nbytes,), 0xFF, dtype=torch.uint8, device="cuda")
+    call(dl, mx4, H.cuda(), M.cuda(), dl.Mx4Matrix.quantize(W.cuda()) if mx4 else W.cuda(),
+         dl.LogitRules(B, L, V, **dev), ALL, o, ws)
+    assert dl.get_status() == 0 and int(o["count"][0]) == B * L
+    check(o, r, V, ALL)

@@ -941,6 +941,8 @@ class DecodeStep:
         if rules is not None or self.weights == "mx4":
             if tuple(M.shape) != (self.B, self.L):
                 raise ValueError(f"M: expected shape ({self.B}, {self.L}), got {tuple(M.shape)}")
+            if block_only and (win_lo is None or win_hi is None):
+                raise ValueError("block_only=True needs win_lo and win_hi")
             (masked_logits_mx4 if self.weights == "mx4" else masked_logits_rules)(
                 H, M, W, rules, self.stats, self.tok, self.conf, self.lse, self.entropy, self.margin,
                 self.row_idx, self.seq_off, self.count, self.ws, stream,

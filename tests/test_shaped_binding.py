@@ -333,3 +333,18 @@ def test_rows_of_another_length_are_refused(fake):                       # noqa:
     assert fake.calls == []
     dl.token_counts(tokens, counts, seen, M=torch.zeros(B * 7, dtype=torch.uint8), stream=S)
     dl.LogitRules(B, L, V, **dict(tables(), allow_id=torch.zeros(N, dtype=torch.int32)))
+
+
+def test_block_only_needs_its_windows(fake):                             # noqa: F811
+    """Without them the step would compute every masked row."""
+    fake.dllm_workspace_bytes_mx4 = lambda *a: 4096
+    b = bufs()
+    rules = dl.LogitRules(B, L, V, bias=torch.zeros(V))
+    for step, W, kw in ((dl.DecodeStep(B, L, d, V, 4, device="cpu"), b["W"], dict(rules=rules)),
+                        (dl.DecodeStep(B, L, d, V, 4, device="cpu", weights="mx4"), dl.Mx4Matrix(b["q"], b["s"]), {})):
+        for win in ((None, None), (b["lo"], None), (None, b["hi"])):
+            with pytest.raises(ValueError, match="block_only=True needs"):
+                step.run(b["H"], b["M"], W, *win, stream=S, block_only=True, **kw)
+        assert fake.calls == []
+        step.run(b["H"], b["M"], W, b["lo"], b["hi"], stream=S, block_only=True, **kw)
+        fake.calls.clear()

@@ -904,3 +904,58 @@ def test_larger_problems(dl, B, L, d, V, mx4):
          dl.LogitRules(B, L, V, **dev), ALL, o, ws)
     assert dl.get_status() == 0 and int(o["count"][0]) == B * L
     check(o, r, V, ALL)
+
+
+@pytest.mark.parametrize("weights", ["bf16", "mx4"])
+@pytest.mark.parametrize("B,L", [(2, 40), (3, 3000)], ids=["staged", "compacted"])
+def test_steps_that_follow_each_other_at_once(dl, weights, B, L):
+    """Steps whose penalties read what the step before has just counted, queued without a pause and
+    replayed from one graph: the selections of the same steps taken one at a time."""
+    d, V, k, steps = 128, 5003, 8, 24
+    H, M, W = head_inputs(B, L, d, V, "none", seed=4)
+    M[:, 5:L:L // 30] = 1
+    Hd, Md = H.cuda(), M.cuda()
+    Wd = dl.Mx4Matrix.quantize(W.cuda()) if weights == "mx4" else W.cuda()
+    counts, seen = i32(B, V), i32(B, (V + 31) // 32)
+    pen = {n: torch.full((B,), v, device="cuda") for n, v in
+           (("repetition", 1.2), ("presence", 0.3), ("frequency", 0.5))}
+    rules = dl.LogitRules(B, L, V, counts=counts, seen=seen, **pen)
+    step = dl.DecodeStep(B, L, d, V, k, weights=weights)
+
+    def start():
+        dl.token_counts(torch.empty(B, 0, dtype=torch.int32, device="cuda"), counts, seen)
+
+    def once():
+        step.run(Hd, Md, Wd, rules=rules)
+        dl.token_counts(step.tok_sel, counts, seen, n_valid=step.n_sel, accumulate=True)
+
+    start()
+    want = []
+    for _ in range(steps):
+        step.run(Hd, Md, Wd, rules=rules)
+        torch.cuda.synchronize()
+        dl.token_counts(step.tok_sel, counts, seen, n_valid=step.n_sel, accumulate=True)
+        torch.cuda.synchronize()
+        want.append(step.sel_buf.clone())
+    last = counts.clone()
+    assert len({tuple(w.tolist()) for w in want}) > steps // 2     # the penalties do change them
+    for _ in range(3):
+        start()
+        got = []
+        for _ in range(steps):
+            once()
+            got.append(step.sel_buf.clone())
+        assert all(torch.equal(a, b) for a, b in zip(got, want)) and torch.equal(counts, last)
+        start()
+        for _ in range(steps):                       # nothing of another library between the kernels
+            once()
+        assert torch.equal(step.sel_buf, want[-1]) and torch.equal(counts, last)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(4):
+            once()
+    start()
+    for _ in range(steps // 4):
+        graph.replay()
+    assert torch.equal(step.sel_buf, want[-1]) and torch.equal(counts, last)
+    assert dl.get_status() == 0

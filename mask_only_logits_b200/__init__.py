@@ -639,8 +639,12 @@ def mx4_dequantize(q, s, X, stream=None) -> None:
 
 
 def mx4_tile_scales(scales: torch.Tensor) -> torch.Tensor:
-    """Row-major E8M0 scales [rows, cols / 32] (as MXFP4 checkpoints store them) in the
-    library's tiles of 128 rows x 4 blocks."""
+    """Row-major E8M0 scales [rows, cols / 32] (as MXFP4 checkpoints store them: bytes, or torch's
+    float8_e8m0fnu) in the library's tiles of 128 rows x 4 blocks."""
+    if scales.dtype == torch.float8_e8m0fnu:
+        scales = scales.view(torch.uint8)
+    if scales.dtype != torch.uint8:
+        raise ValueError(f"scales: expected torch.uint8 or torch.float8_e8m0fnu, got {scales.dtype}")
     rows, blocks = scales.shape
     R, G = -(-rows // 128), -(-blocks // 4)
     full = torch.zeros(R * 128, G * 4, dtype=torch.uint8, device=scales.device)

@@ -348,3 +348,15 @@ def test_block_only_needs_its_windows(fake):                             # noqa:
         assert fake.calls == []
         step.run(b["H"], b["M"], W, b["lo"], b["hi"], stream=S, block_only=True, **kw)
         fake.calls.clear()
+
+
+def test_scale_tiles_take_bytes_or_e8m0():
+    """A checkpoint's scales as torch's E8M0 numbers are the same bytes, not their values rounded to
+    integers; other types are refused."""
+    g = torch.arange(3 * 5, dtype=torch.uint8).view(3, 5) * 17
+    want = dl.mx4_tile_scales(g)
+    assert torch.equal(dl.mx4_tile_scales(g.view(torch.float8_e8m0fnu)), want)
+    assert torch.equal(dl.mx4_row_scales(want, 3, 160), g)
+    for t in (torch.int8, torch.int32, torch.float32):
+        with pytest.raises(ValueError, match="scales: expected"):
+            dl.mx4_tile_scales(g.to(t))

@@ -480,8 +480,8 @@ dllm_status dllm_decode_block_step(const uint16_t* H, const uint8_t* M, const ui
  *   counts      device int32 [B] rows of V, counts_stride apart (>= V): how often each token
  *               stands in each sequence (dllm_token_counts).
  *   seen        device bitmap of counts > 0: bit v % 32 of word v / 32, rows seen_stride words
- *               apart (>= ceil(V / 32)).  Required with counts; counts are read only where its
- *               bit is set.
+ *               apart (>= ceil(V / 32)).  Required with counts; counts matter only where its
+ *               bit is set (the others may hold anything, but are read).
  *   repetition, presence, frequency   device float32 [B]; repetition > 0.  They require counts.
  *   allow       device bitmaps of allowed tokens: allow_rows rows of ceil(V / 32) words,
  *               allow_stride words apart; bit set = allowed.
@@ -493,6 +493,8 @@ dllm_status dllm_decode_block_step(const uint16_t* H, const uint8_t* M, const ui
  * A row with no token left (every z = -infinity): tok = -1, conf = 0, lse = -infinity,
  * entropy = +infinity, margin = -0.  A selection by one of these scores takes such a row after
  * all others (a row whose two best logits are equal has margin +0, which orders above -0).
+ * A row with a NaN among its allowed logits: conf, lse and the scores are NaN, and tok is some
+ * number in [0, V); a selection does not take NaN scores.
  */
 typedef struct dllm_logit_rules {
   const float* bias;

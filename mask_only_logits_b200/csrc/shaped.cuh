@@ -28,12 +28,19 @@
 //             tiles and about 0.62 of them: frequent tokens sit at the low ids of a vocabulary,
 //             so a stream of consecutive tiles would get all the penalised columns (99 us where
 //             the others took 65, 256 rows of d2048 V151936).
-//   sums      The tensor cores drop what does not fit fp32 at every addition (K = 16), always
+//   sums      The tensor cores drop what does not fit fp32 beside the running sum, always
 //             towards zero: over d = 4096 a large bf16 logit came out 5e-6 too small.  An
 //             accumulator therefore holds a piece of K; the epilogue adds the pieces up in
-//             registers (128 a thread, dealt to the epilogue's warpgroups by setmaxnreg), which
-//             leaves about an fp32 sum's error (0.1e-6 to 1.4e-6).  MXFP4 products are a few
-//             bits wide and their sums exact.
+//             registers (128 a thread, dealt to the epilogue's warpgroups by setmaxnreg).  Of a
+//             normal row's statistics that leaves an fp32 sum's error (d up to 4096: 0.1e-6 to
+//             1.5e-6).  Where a few channels make most of a sum and the rest add to it with one
+//             sign, the piece that holds them loses about 1.4 last places per step of K = 16:
+//             with the largest 2^10 times the others, d = 4096, pairs are 9e-6 off, single CTAs
+//             0.8e-6, a rounded fp32 sum 0.7e-6.
+//             MXFP4 products are a few bits wide: their sums are exact while the scales of the
+//             blocks that matter lie close together.  With scales drawn from 2^-12 to 2^12 the
+//             d / 64 steps truncate too: 0.8e-6 at d = 2048, 1.5e-6 at 4096, 2.7e-6 at 8192 (a
+//             rounded fp32 sum 0.9e-6, 1.1e-6, 2.1e-6), so a tile's K stays in one accumulator.
 //   epilogue  eight warps: two per TMEM lane quadrant, each with half of a tile's columns (the
 //             rules and scores cost more instructions than the plain statistics, and four MXFP4
 //             tiles take the time of one bf16 tile).  rules on each 32 logits, then
@@ -368,9 +375,10 @@ __device__ __forceinline__ void run(uint8_t* smem_raw, const Maps& tm, int count
   // of K 185, with 512 178, unsplit 173), and a call on few rows has no others for its error to
   // average with: of 40 random calls of 1 to 128 rows 5 came out more than 1e-6 off (256: 8, 512:
   // 13), as many as with plain fp32 sums.
-  // Pairs: a quarter of K, at least 512: with it the error stays by that of an fp32 sum, which
-  // grows with K too.  256 rows d2048 V151936 with all rules: 512 219 us, 768 209, 1024 188,
-  // unsplit 173; 1024 rows d4096 V126464: 907, 876, 832, 800 us (both under the power cap).
+  // Pairs: a quarter of K, at least 512: with it a normal row's error stays by that of an fp32 sum,
+  // which grows with K too (d = 1024, 2048, 4096, 8192: 0.7, 0.7, 1.2, 2.7e-6; fp32 0.7, 0.7, 1.8,
+  // 2.3e-6).  256 rows d2048 V151936 with all rules: 512 219 us, 768 209, 1024 188, unsplit 173;
+  // 1024 rows d4096 V126464: 907, 876, 832, 800 us (both under the power cap).
   int piece_stages = KB;
   if (!Op::kMx4) {
     const int quarter = (KB + 3) / 4;
